@@ -285,6 +285,104 @@ pwp_status pwp_sweep_buffers(const pwp_sweep* sweep, uint32_t** level1, int64_t*
 pwp_status pwp_pack_24(const float* W_hat_dev, const uint8_t* mask_dev, int32_t c, int32_t b,
                        uint16_t* values_dev, uint32_t* meta_dev, pwp_stats* stats_dev, void* stream);
 
+/* ---- Forward pass of a decoder block on the calibration tokens.
+ *
+ * "Pruning LLMs with Thanos", section "Thanos versus SparseGPT on LLaMA-3 8B", runs calibration
+ * sequences through the model to get each layer's X; these are the block's operators.
+ * Rows are tokens.  Every tensor has contiguous elements inside a row (a head, for q, k and v)
+ * and strides in elements between rows, tokens and heads, so slices of a packed projection
+ * output can be passed as they are; no alignment beyond the element's own is needed (16-byte
+ * aligned bases and strides take the fast kernels).  type is PWP_BF16 or PWP_FP32, the same
+ * for every tensor of a call; sums are fp32 and each output is rounded once to its type.
+ * A call with no rows enqueues nothing.  No workspace.  stats_dev (linear, attention) is
+ * optional: it receives device-side errors and is not cleared by the call; without it a
+ * wait that runs out leaves NaN in the rows it was to write. */
+
+/* out = x / sqrt(mean(x^2) + eps) * weight, over rows of `width` (1 <= width <= 65536).
+ * weight_dev: `width` elements of `type`, or NULL.  out may be x itself (same stride). */
+pwp_status pwp_rms_norm(const void* x_dev, int32_t type, int64_t rows, int32_t width, int64_t x_stride,
+                        const void* weight_dev, float eps, void* out_dev, int64_t out_stride, void* stream);
+
+/* Queries and keys of n tokens: each head x (d elements) is normalised, x / sqrt(mean(x^2) +
+ * eps) * weight, when its weight is given, and its first `rot` elements are turned by the
+ * token's position: pair i (of rot/2) by the angle position * freqs[i], cosine and sine
+ * multiplied by `factor`.  The angle is formed and reduced in double precision, so far
+ * positions keep their accuracy.  layout PWP_ROPE_HALF pairs elements i and i + rot/2,
+ * PWP_ROPE_INTERLEAVED 2i and 2i+1; elements from `rot` on are only normalised.
+ *   1 <= d <= 1024, 0 <= rot <= d, rot even; hq, hk >= 0 (hk 0: no keys).
+ *   q_out / k_out may be q / k themselves (same strides). */
+typedef enum { PWP_ROPE_HALF = 0, PWP_ROPE_INTERLEAVED = 1 } pwp_rope_layout;
+typedef struct {
+    const void* q_dev;           /* [n][hq][d] */
+    const void* k_dev;           /* [n][hk][d] */
+    void* q_out_dev;
+    void* k_out_dev;
+    int64_t q_stride[2];         /* token, head */
+    int64_t k_stride[2];
+    int64_t q_out_stride[2];
+    int64_t k_out_stride[2];
+    const int64_t* positions_dev;   /* n */
+    const double* freqs_dev;        /* rot / 2 */
+    const void* q_weight_dev;       /* d, or NULL: q is not normalised */
+    const void* k_weight_dev;       /* d, or NULL: k is not normalised */
+    int64_t n;
+    int32_t type, hq, hk, d, rot, layout;
+    float eps, factor;
+} pwp_rope_args;
+pwp_status pwp_qk_norm_rope(const pwp_rope_args* args, void* stream);
+
+/* Attention within each of nseq packed sequences: rows cu_seqlens[s] .. cu_seqlens[s+1] are
+ * sequence s, and query i of head h gets sum_j softmax_j(scale * q_i k_j) v_j over the keys of
+ * its own sequence (causal: those at or before i) of head h / (hq / hk).
+ *   cu_seqlens_dev : nseq + 1 offsets, not decreasing, within 0 .. n, read on the device; the
+ *                    first sequence whose two offsets break this and all behind it are
+ *                    skipped and, with stats_dev, reported as PWP_EINVAL.
+ *   hq a multiple of hk; 1 <= d <= 256; n * hq < 2^31.
+ * Rows outside every sequence are left as they were.  out must not overlap q, k or v.
+ * Non-finite values of another sequence, of rows behind the last one, or of a later token
+ * (causal) do not reach a query. */
+typedef struct {
+    const void* q_dev;           /* [n][hq][d] */
+    const void* k_dev;           /* [n][hk][d] */
+    const void* v_dev;           /* [n][hk][d] */
+    void* out_dev;               /* [n][hq][d] */
+    int64_t q_stride[2];         /* token, head */
+    int64_t k_stride[2];
+    int64_t v_stride[2];
+    int64_t out_stride[2];
+    const int32_t* cu_seqlens_dev;
+    pwp_stats* stats_dev;        /* or NULL */
+    int64_t n;
+    int32_t nseq, type, hq, hk, d, causal;
+    float scale;
+} pwp_attention_args;
+pwp_status pwp_attention(const pwp_attention_args* args, void* stream);
+
+/* out = act(x W^T + bias) + residual, or with w_up_dev the gated product
+ * out = act(x W^T + bias) * (x W_up^T + bias_up) + residual.
+ *   x [rows][k], W and W_up [n][k], out and residual [rows][n]; biases n elements;
+ *   bias, bias_up and residual may be NULL; residual may be out itself (same stride).
+ *   1 <= k, n < 2^24; rows < 2^31.  out overlaps nothing else.
+ * Activations: x; max(x, 0); x / (1 + e^-x); x Phi(x) with Phi the normal distribution; the
+ * same with Phi(x) as (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2. */
+typedef enum {
+    PWP_ACT_NONE = 0, PWP_ACT_RELU = 1, PWP_ACT_SILU = 2, PWP_ACT_GELU = 3, PWP_ACT_GELU_TANH = 4
+} pwp_activation;
+typedef struct {
+    const void* x_dev;
+    const void* w_dev;
+    const void* w_up_dev;        /* or NULL */
+    const void* bias_dev;        /* or NULL */
+    const void* bias_up_dev;     /* or NULL */
+    const void* residual_dev;    /* or NULL */
+    void* out_dev;
+    int64_t x_stride, w_stride, w_up_stride, residual_stride, out_stride;
+    pwp_stats* stats_dev;        /* or NULL */
+    int64_t rows;
+    int32_t k, n, type, activation;
+} pwp_linear_args;
+pwp_status pwp_linear(const pwp_linear_args* args, void* stream);
+
 /* Prune without a caller-provided workspace (the pages have no counterpart: this is a
  * convenience of this library).  For callers that cannot allocate device memory when
  * they call -- an operator in a runtime that hands it only its input and output

@@ -7,7 +7,9 @@ missing, loading it raises.
 
 Names mirror the C entry points: ``hessian_accumulate``, ``damp_factor``,
 ``prune_layer`` (H given or built from X), ``workspace_bytes``, plus
-``prune_layer_host`` for a call that starts and ends in host memory.
+``prune_layer_host`` for a call that starts and ends in host memory.  The forward pass of a
+decoder block on calibration tokens (``block_forward`` and its operators, ``attention``,
+``linear``, ...) is in ``block``.
 """
 from __future__ import annotations
 
@@ -23,6 +25,8 @@ __all__ = [
     "lib", "Config", "Stats", "THANOS", "SPARSEGPT", "WANDA", "MAGNITUDE", "UNSTRUCTURED", "NM", "BF16", "FP32",
     "PwpError", "config", "workspace_bytes", "hessian_accumulate", "damp_factor", "prune_layer",
     "prune_layer_host", "prune_block", "pack_24", "status_string", "set_wait_limit", "Sweep", "LIB_PATH",
+    "rms_norm", "rope_frequencies", "qk_norm_rope", "attention", "linear", "gated_linear", "block_forward",
+    "prune_decoder_block", "FEEDS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpwp.so")
@@ -94,7 +98,7 @@ def lib():
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"libpwp.so not built ({LIB_PATH}); run python -m post_weight_pruning_b200.build")
         L = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in _SIGS.items():
+        for name, (res, args) in {**_SIGS, **_block.SIGNATURES}.items():
             f = getattr(L, name)
             f.restype = res
             f.argtypes = args
@@ -570,3 +574,8 @@ def from_bf16_bits(u16: np.ndarray, device="cuda"):
     torch = _torch()
     t = torch.from_numpy(np.ascontiguousarray(u16).view(np.int16))
     return t.view(torch.bfloat16).to(device)
+
+
+from . import block as _block  # noqa: E402
+from .block import (FEEDS, attention, block_forward, gated_linear, linear, prune_decoder_block,  # noqa: E402
+                    qk_norm_rope, rms_norm, rope_frequencies)

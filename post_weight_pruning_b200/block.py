@@ -1,0 +1,467 @@
+"""Forward pass of a decoder block on calibration tokens: the operators that turn a block's
+hidden states into the activations its layers are pruned with.
+
+``rms_norm``, ``qk_norm_rope``, ``attention``, ``linear`` and ``gated_linear`` marshal their
+arguments to the C entry points of the same names (include/pwp.h); ``rope_frequencies`` forms
+the rotation's frequencies.  ``block_forward`` runs them as a decoder block and returns every
+distinct layer input beside the block's output, and ``prune_decoder_block`` prunes the block
+with those inputs and passes the hidden states through the pruned layers.
+
+The operators run on the device of their tensors and on the given or the current stream of
+that device; nothing synchronises and nothing is kept between calls.  They compute a forward
+pass only: an input that requires a gradient is refused while gradients are recorded.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+import inspect
+import math
+
+import numpy as np
+
+import post_weight_pruning_b200 as _pwp
+
+_vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+LAYOUTS = {"half": 0, "interleaved": 1}
+# the layer input each projection of a decoder block reads
+FEEDS = {"q_proj": "attn_in", "k_proj": "attn_in", "v_proj": "attn_in", "o_proj": "o_in", "gate_proj": "mlp_in",
+         "up_proj": "mlp_in", "down_proj": "down_in"}
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("q_out", _vp), ("k_out", _vp), ("q_stride", _i64 * 2), ("k_stride", _i64 * 2),
+                ("q_out_stride", _i64 * 2), ("k_out_stride", _i64 * 2), ("positions", _vp), ("freqs", _vp),
+                ("q_weight", _vp), ("k_weight", _vp), ("n", _i64), ("type", _i32), ("hq", _i32), ("hk", _i32),
+                ("d", _i32), ("rot", _i32), ("layout", _i32), ("eps", _f32), ("factor", _f32)]
+
+
+class AttentionArgs(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("out", _vp), ("q_stride", _i64 * 2), ("k_stride", _i64 * 2),
+                ("v_stride", _i64 * 2), ("out_stride", _i64 * 2), ("cu_seqlens", _vp), ("stats", _vp), ("n", _i64),
+                ("nseq", _i32), ("type", _i32), ("hq", _i32), ("hk", _i32), ("d", _i32), ("causal", _i32),
+                ("scale", _f32)]
+
+
+class LinearArgs(ctypes.Structure):
+    _fields_ = [("x", _vp), ("w", _vp), ("w_up", _vp), ("bias", _vp), ("bias_up", _vp), ("residual", _vp),
+                ("out", _vp), ("x_stride", _i64), ("w_stride", _i64), ("w_up_stride", _i64),
+                ("residual_stride", _i64), ("out_stride", _i64), ("stats", _vp), ("rows", _i64), ("k", _i32),
+                ("n", _i32), ("type", _i32), ("activation", _i32)]
+
+
+SIGNATURES = {
+    "pwp_rms_norm": (_i32, [_vp, _i32, _i64, _i32, _i64, _vp, _f32, _vp, _i64, _vp]),
+    "pwp_qk_norm_rope": (_i32, [ctypes.POINTER(RopeArgs), _vp]),
+    "pwp_attention": (_i32, [ctypes.POINTER(AttentionArgs), _vp]),
+    "pwp_linear": (_i32, [ctypes.POINTER(LinearArgs), _vp]),
+}
+
+
+# ------------------------------------------------------------------- argument checks
+
+def _operator(fn):
+    """Run an operator on the device of its first tensor, and on the given stream of that
+    device when there is one."""
+    on_stream = _pwp._on_stream(fn)
+    first = next(iter(inspect.signature(fn).parameters))
+
+    @functools.wraps(fn)
+    def wrapped(*a, **kw):
+        torch = _pwp._torch()
+        x = a[0] if a else kw.get(first)
+        if not torch.is_tensor(x):
+            raise TypeError(f"{fn.__name__}: {first}: tensor expected, got {type(x).__name__}")
+        call = fn if kw.get("stream") is None else on_stream
+        if not x.is_cuda or x.device.index == torch.cuda.current_device():
+            return call(*a, **kw)
+        with torch.cuda.device(x.device):
+            return call(*a, **kw)
+    return wrapped
+
+
+def _check_tensor(t, name, shape, like, dtype=None):
+    """`t` on the device of `like`, of its element type (or `dtype`) and of `shape`, with
+    contiguous elements in its last dimension."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != (dtype or like.dtype):
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype or like.dtype}")
+    if t.device != like.device:
+        raise ValueError(f"{name}: on {t.device}, the first tensor on {like.device}")
+    if t.shape and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: elements of the last dimension must be contiguous")
+
+
+def _check_first(t, name, dims):
+    _pwp._dtype_code(t)
+    if t.dim() != dims:
+        raise ValueError(f"{name}: {dims} dimensions expected, got shape {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: CUDA tensors expected")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: elements of the last dimension must be contiguous")
+
+
+def _check_out(t, name, shape, like):
+    """An output given by the caller: no two of its elements in one place."""
+    _check_tensor(t, name, shape, like)
+    reach = 1
+    for stride, size in sorted((t.stride(i), t.shape[i]) for i in range(t.dim()) if t.shape[i] > 1):
+        if stride < reach:
+            raise ValueError(f"{name}: elements overlap (shape {tuple(t.shape)}, strides {t.stride()})")
+        reach = stride * size
+
+
+def _forward_only(*ts):
+    torch = _pwp._torch()
+    if torch.is_grad_enabled():
+        for t in ts:
+            if t is not None and t.requires_grad:
+                raise ValueError("the operators compute a forward pass only: call them under torch.no_grad() "
+                                 "or on detached tensors")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stats_ptr(stats, like):
+    if stats is not None:
+        torch = _pwp._torch()
+        _check_tensor(stats, "stats", (ctypes.sizeof(_pwp.Stats),), like, torch.uint8)
+    return _ptr(stats)
+
+
+def _call(name, args):
+    st = getattr(_pwp.lib(), name)(ctypes.byref(args), _pwp._stream_ptr())
+    if st:
+        raise _pwp.PwpError(st, name)
+
+
+# ------------------------------------------------------------------- operators
+
+@_operator
+def rms_norm(x, weight=None, *, eps=1e-5, out=None, stream=None):
+    """x / sqrt(mean(x^2) + eps) * weight over the rows of x ([n, width], bf16 or fp32;
+    rows may be strided).  weight: [width] or None.  out: None, a tensor like x, or x itself."""
+    torch = _pwp._torch()
+    _check_first(x, "x", 2)
+    n, width = x.shape
+    if width < 1 or width > 65536:
+        raise ValueError(f"x: width {width}, 1 to 65536 expected")
+    if weight is not None:
+        _check_tensor(weight, "weight", (width,), x)
+    if not (eps >= 0 and math.isfinite(eps)):
+        raise ValueError(f"eps: {eps}")
+    _forward_only(x, weight)
+    if out is None:
+        out = torch.empty((n, width), dtype=x.dtype, device=x.device)
+    elif out is not x:
+        _check_out(out, "out", (n, width), x)
+    if n:
+        st = _pwp.lib().pwp_rms_norm(x.data_ptr(), _pwp._dtype_code(x), n, width, x.stride(0), _ptr(weight),
+                                     float(eps), out.data_ptr(), out.stride(0), _pwp._stream_ptr())
+        _pwp._check(st, "pwp_rms_norm")
+    return out
+
+
+def rope_frequencies(rot, *, base=10000.0, scaling=None, device="cuda"):
+    """(frequencies, factor) of the rotation of `rot` elements (even) for qk_norm_rope: a
+    double-precision tensor [rot / 2] on `device`, f_i = base^(-2 i / rot), and the number
+    cosine and sine are multiplied by.  scaling stretches them to longer contexts:
+      None                                   as they are, factor 1
+      {"type": "linear", "factor": s}        f_i / s: positions closer together
+      {"type": "base", "factor": s}          the base times s^(rot / (rot - 2)): the slowest
+                                             pair s times slower, the fastest unchanged
+      {"type": "bands", "factor": s, "low_freq_factor": l, "high_freq_factor": h,
+       "original_max_positions": n0}         pairs that make fewer than l turns over n0
+                                             positions slowed by s, those with more than h
+                                             unchanged, linear between (in turns)
+      {"type": "yarn", "factor": s, "original_max_positions": n0, "beta_fast": 32.0,
+       "beta_slow": 1.0}                     the same idea with the ramp linear in the pair's
+                                             index, between the pairs that make beta_fast and
+                                             beta_slow turns; factor 0.1 ln s + 1"""
+    torch = _pwp._torch()
+    rot = int(rot)
+    if rot < 0 or rot % 2 or not base > 0:
+        raise ValueError(f"rot even and base > 0 expected, got {rot} and {base}")
+    i = np.arange(0, rot, 2, dtype=np.float64)
+    f = float(base) ** (-i / max(rot, 1))
+    factor = 1.0
+    if scaling is not None:
+        sc = dict(scaling)
+        kind, s = sc.pop("type", None), float(sc.pop("factor", 0.0))
+        if not s > 0:
+            raise ValueError(f"scaling: factor > 0 expected, got {scaling}")
+        if kind == "linear":
+            f = f / s
+        elif kind == "base":
+            if rot <= 2:
+                raise ValueError("scaling by the base needs rot > 2")
+            f = (float(base) * s ** (rot / (rot - 2))) ** (-i / rot)
+        elif kind == "bands":
+            lo, hi = float(sc.pop("low_freq_factor")), float(sc.pop("high_freq_factor"))
+            n0 = float(sc.pop("original_max_positions"))
+            if not hi > lo:
+                raise ValueError("scaling: high_freq_factor > low_freq_factor expected")
+            keep = np.clip((n0 * f / (2 * math.pi) - lo) / (hi - lo), 0.0, 1.0)
+            f = f * (keep + (1.0 - keep) / s)
+        elif kind == "yarn":
+            n0 = float(sc.pop("original_max_positions"))
+            fast, slow = float(sc.pop("beta_fast", 32.0)), float(sc.pop("beta_slow", 1.0))
+            pair = lambda turns: rot * math.log(n0 / (turns * 2 * math.pi)) / (2 * math.log(base))
+            lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rot - 1)
+            slowed = np.clip((np.arange(rot // 2) - lo) / max(hi - lo, 1e-3), 0.0, 1.0)
+            f = f * (1.0 - slowed) + f / s * slowed
+            factor = 0.1 * math.log(s) + 1.0
+        else:
+            raise ValueError(f"scaling: unknown type {kind!r}")
+        if sc:
+            raise ValueError(f"scaling: unknown entries {sorted(sc)}")
+    return torch.from_numpy(np.ascontiguousarray(f, dtype=np.float64)).to(device), factor
+
+
+@_operator
+def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e-5, layout="half", factor=1.0,
+                 q_out=None, k_out=None, stream=None):
+    """Queries and keys of n tokens, normalised per head and turned by position in one pass.
+
+    q: [n, hq, d], k: [n, hk, d] (bf16 or fp32; token and head strides free, so slices of a
+    packed projection output do); positions: int64 [n]; freqs, factor: from
+    ``rope_frequencies`` (the first 2 * len(freqs) elements of a head are turned).
+    q_weight, k_weight: [d], the head norms' weights, or None for no norm.  layout "half" pairs
+    elements i and i + rot/2, "interleaved" 2i and 2i+1.  q_out / k_out: None, tensors of the
+    same shapes, or q / k themselves.  Returns (q_out, k_out)."""
+    torch = _pwp._torch()
+    _check_first(q, "q", 3)
+    n, hq, d = q.shape
+    if k.dim() != 3:
+        raise ValueError(f"k: [n, heads, d] expected, got shape {tuple(k.shape)}")
+    hk = k.shape[1]
+    _check_tensor(k, "k", (n, hk, d), q)
+    _check_tensor(positions, "positions", (n,), q, torch.int64)
+    if freqs.dim() != 1:
+        raise ValueError(f"freqs: one dimension expected, got shape {tuple(freqs.shape)}")
+    rot = 2 * freqs.shape[0]
+    _check_tensor(freqs, "freqs", (rot // 2,), q, torch.float64)
+    if not 1 <= d <= 1024 or rot > d:
+        raise ValueError(f"head size {d} (1 to 1024), {rot} elements turned")
+    if layout not in LAYOUTS:
+        raise ValueError(f"layout: {layout!r}, one of {sorted(LAYOUTS)} expected")
+    if not (eps >= 0 and math.isfinite(eps) and math.isfinite(factor)):
+        raise ValueError(f"eps {eps}, factor {factor}")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _check_tensor(w, name, (d,), q)
+    _forward_only(q, k, q_weight, k_weight)
+    if q_out is None:
+        q_out = torch.empty((n, hq, d), dtype=q.dtype, device=q.device)
+    elif q_out is not q:
+        _check_out(q_out, "q_out", (n, hq, d), q)
+    if k_out is None:
+        k_out = torch.empty((n, hk, d), dtype=q.dtype, device=q.device)
+    elif k_out is not k:
+        _check_out(k_out, "k_out", (n, hk, d), q)
+    if n and hq + hk:
+        if positions.stride(0) != 1 and n > 1:
+            raise ValueError("positions: contiguous tensor expected")
+        two = _i64 * 2
+        _call("pwp_qk_norm_rope", RopeArgs(
+            q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), two(q.stride(0), q.stride(1)),
+            two(k.stride(0), k.stride(1)), two(q_out.stride(0), q_out.stride(1)),
+            two(k_out.stride(0), k_out.stride(1)), positions.data_ptr(), freqs.data_ptr(), _ptr(q_weight),
+            _ptr(k_weight), n, _pwp._dtype_code(q), hq, hk, d, rot, LAYOUTS[layout], eps, factor))
+    return q_out, k_out
+
+
+@_operator
+def attention(q, k, v, cu_seqlens, *, causal=True, scale=None, out=None, stats=None, stream=None):
+    """Softmax attention within each of the packed sequences.
+
+    q: [n, hq, d], k and v: [n, hk, d] (bf16 or fp32, d <= 256, hq a multiple of hk; token and
+    head strides free); cu_seqlens: int32 [sequences + 1] on the device: sequence s is rows
+    cu_seqlens[s] to cu_seqlens[s+1].  scale: default 1 / sqrt(d).  Returns out [n, hq, d];
+    rows in no sequence are left as they were (of a fresh output: undefined).  Offsets that
+    decrease or leave 0..n end the batch there and set status 1 in `stats` (a ``new_stats``
+    record, optional), which also receives a device-side wait that ran out."""
+    torch = _pwp._torch()
+    _check_first(q, "q", 3)
+    n, hq, d = q.shape
+    if k.dim() != 3:
+        raise ValueError(f"k: [n, heads, d] expected, got shape {tuple(k.shape)}")
+    hk = k.shape[1]
+    _check_tensor(k, "k", (n, hk, d), q)
+    _check_tensor(v, "v", (n, hk, d), q)
+    if hk < 1 or hq < 1 or hq % hk:
+        raise ValueError(f"{hq} query heads do not divide among {hk} key heads")
+    if not 1 <= d <= 256:
+        raise ValueError(f"head size {d}, 1 to 256 expected")
+    if n * hq >= 1 << 31:
+        raise ValueError(f"{n} tokens of {hq} heads: fewer than 2^31 query rows expected")
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError(f"cu_seqlens: [sequences + 1] expected, got shape {tuple(cu_seqlens.shape)}")
+    _check_tensor(cu_seqlens, "cu_seqlens", cu_seqlens.shape, q, torch.int32)
+    if scale is None:
+        scale = d ** -0.5
+    if not math.isfinite(scale):
+        raise ValueError(f"scale: {scale}")
+    _forward_only(q, k, v)
+    stats_p = _stats_ptr(stats, q)
+    if out is None:
+        out = torch.empty((n, hq, d), dtype=q.dtype, device=q.device)
+    else:
+        _check_out(out, "out", (n, hq, d), q)
+    nseq = cu_seqlens.shape[0] - 1
+    if n and nseq:
+        two = _i64 * 2
+        _call("pwp_attention", AttentionArgs(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), two(q.stride(0), q.stride(1)),
+            two(k.stride(0), k.stride(1)), two(v.stride(0), v.stride(1)), two(out.stride(0), out.stride(1)),
+            cu_seqlens.data_ptr(), stats_p, n, nseq, _pwp._dtype_code(q), hq, hk, d, 1 if causal else 0, scale))
+    return out
+
+
+def _linear(x, w, w_up, bias, bias_up, activation, residual, out, stats, name):
+    torch = _pwp._torch()
+    _check_first(x, "x", 2)
+    rows, k = x.shape
+    if w.dim() != 2:
+        raise ValueError(f"{name}: [n, k] expected, got shape {tuple(w.shape)}")
+    n = w.shape[0]
+    _check_tensor(w, name, (n, k), x)
+    if not (1 <= k < 1 << 24 and 1 <= n < 1 << 24 and rows < 1 << 31):
+        raise ValueError(f"sizes out of range: {rows} rows, k {k}, n {n}")
+    if w_up is not None:
+        _check_tensor(w_up, "w_up", (n, k), x)
+    for nm, b in (("bias", bias), ("bias_up", bias_up)):
+        if b is not None:
+            _check_tensor(b, nm, (n,), x)
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation: {activation!r}, one of {sorted(ACTIVATIONS)} expected")
+    if residual is not None:
+        _check_tensor(residual, "residual", (rows, n), x)
+    _forward_only(x, w, w_up, bias, bias_up, residual)
+    stats_p = _stats_ptr(stats, x)
+    if out is None:
+        out = torch.empty((rows, n), dtype=x.dtype, device=x.device)
+    else:
+        _check_out(out, "out", (rows, n), x)
+    if rows:
+        _call("pwp_linear", LinearArgs(
+            x.data_ptr(), w.data_ptr(), _ptr(w_up), _ptr(bias), _ptr(bias_up), _ptr(residual), out.data_ptr(),
+            x.stride(0), w.stride(0), w_up.stride(0) if w_up is not None else 0,
+            residual.stride(0) if residual is not None else 0, out.stride(0), stats_p, rows, k, n,
+            _pwp._dtype_code(x), ACTIVATIONS[activation]))
+    return out
+
+
+@_operator
+def linear(x, w, *, bias=None, activation="none", residual=None, out=None, stats=None, stream=None):
+    """activation(x w^T + bias) + residual for x [rows, k], w [n, k], bias [n] and residual
+    [rows, n] (bf16 or fp32, one type; rows may be strided).  activation: "none", "relu",
+    "silu", "gelu" (by the normal distribution) or "gelu_tanh".  out: None or a tensor
+    [rows, n], which may be `residual` itself.  stats: an optional ``new_stats`` record for a
+    device-side wait that ran out (without it the rows concerned come out NaN)."""
+    return _linear(x, w, None, bias, None, activation, residual, out, stats, "w")
+
+
+@_operator
+def gated_linear(x, w_gate, w_up, *, bias_gate=None, bias_up=None, activation="silu", out=None, stats=None,
+                 stream=None):
+    """activation(x w_gate^T + bias_gate) * (x w_up^T + bias_up): both projections of a gated
+    feed-forward block, the activation and the product in one kernel.  Shapes, types and the
+    other arguments as for ``linear``."""
+    return _linear(x, w_gate, w_up, bias_gate, bias_up, activation, None, out, stats, "w_gate")
+
+
+# ------------------------------------------------------------------- a decoder block
+
+def block_forward(weights, hidden, seq_lens, *, heads, kv_heads=None, freqs=None, factor=1.0, layout="half",
+                  positions=None, norms=None, biases=None, activation="silu", eps=1e-5, causal=True, scale=None,
+                  stats=None, stream=None):
+    """One decoder block over packed calibration sequences.
+
+    weights: {"q_proj", "k_proj", "v_proj", "o_proj", "gate_proj", "up_proj", "down_proj":
+    [n, k] tensors}; hidden: [tokens, width], the block's input, of the weights' type; seq_lens:
+    the sequences' lengths (they add up to the tokens).  heads / kv_heads: of the queries and
+    of the keys and values (default: the same).  freqs, factor, layout, positions: as for
+    ``qk_norm_rope`` (freqs None: no rotation; positions None: 0, 1, ... in each sequence).
+    norms: {"attn", "mlp": [width] weights of the block's norms, "q", "k": [d] weights of the
+    head norms}, each optional (a missing "attn" or "mlp" norms without a weight, a missing
+    "q" or "k" leaves the heads as they are); biases: {projection: [n]}, each optional.
+
+    Returns (activations, out): {"attn_in", "o_in", "mlp_in", "down_in"}, the inputs of
+    the projections as ``FEEDS`` names them (``prune_block``'s activations), and the block's
+    output, residuals included.  stats: an optional ``new_stats`` record."""
+    torch = _pwp._torch()
+    missing = sorted(set(FEEDS) - set(weights))
+    if missing:
+        raise ValueError(f"weights: {missing} missing")
+    norms, biases = dict(norms or {}), dict(biases or {})
+    for name, given, known in (("norms", norms, {"attn", "mlp", "q", "k"}), ("biases", biases, set(FEEDS))):
+        if set(given) - known:
+            raise ValueError(f"{name}: unknown entries {sorted(set(given) - known)}")
+    if hidden.dim() != 2:
+        raise ValueError(f"hidden: [tokens, width] expected, got shape {tuple(hidden.shape)}")
+    lens = [int(x) for x in seq_lens]
+    n = hidden.shape[0]
+    if any(x < 0 for x in lens) or sum(lens) != n:
+        raise ValueError(f"seq_lens: {sum(lens)} tokens in all, hidden has {n}")
+    kv_heads = heads if kv_heads is None else kv_heads
+    if heads < 1 or kv_heads < 1 or heads % kv_heads or weights["q_proj"].shape[0] % heads:
+        raise ValueError(f"{heads} query heads, {kv_heads} key heads, q_proj {tuple(weights['q_proj'].shape)}")
+    d = weights["q_proj"].shape[0] // heads
+    if stream is not None:
+        with torch.cuda.device(hidden.device), _pwp._stream_ctx(stream):
+            return block_forward(weights, hidden, lens, heads=heads, kv_heads=kv_heads, freqs=freqs, factor=factor,
+                                 layout=layout, positions=positions, norms=norms, biases=biases,
+                                 activation=activation, eps=eps, causal=causal, scale=scale, stats=stats)
+    dev = hidden.device
+    cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32).to(dev)
+    w, b = weights, biases.get
+    attn_in = rms_norm(hidden, norms.get("attn"), eps=eps)
+    packed = torch.empty((n, (heads + 2 * kv_heads) * d), dtype=hidden.dtype, device=dev)
+    ends = np.cumsum([0, heads * d, kv_heads * d, kv_heads * d])
+    q, k, v = (packed[:, ends[i]:ends[i + 1]] for i in range(3))
+    for name, dst in (("q_proj", q), ("k_proj", k), ("v_proj", v)):
+        linear(attn_in, w[name], bias=b(name), out=dst, stats=stats)
+    q, k, v = q.view(n, heads, d), k.view(n, kv_heads, d), v.view(n, kv_heads, d)
+    if freqs is not None or norms.get("q") is not None or norms.get("k") is not None:
+        if freqs is None:
+            freqs = torch.empty(0, dtype=torch.float64, device=dev)
+        if positions is None:
+            positions = torch.from_numpy(np.concatenate([np.arange(x, dtype=np.int64) for x in lens])
+                                         if lens else np.zeros(0, np.int64)).to(dev)
+        qk_norm_rope(q, k, positions, freqs, q_weight=norms.get("q"), k_weight=norms.get("k"), eps=eps, layout=layout,
+                     factor=factor, q_out=q, k_out=k)
+    o_in = attention(q, k, v, cu, causal=causal, scale=scale, stats=stats).view(n, heads * d)
+    mid = linear(o_in, w["o_proj"], bias=b("o_proj"), residual=hidden, stats=stats)
+    mlp_in = rms_norm(mid, norms.get("mlp"), eps=eps)
+    down_in = gated_linear(mlp_in, w["gate_proj"], w["up_proj"], bias_gate=b("gate_proj"), bias_up=b("up_proj"),
+                           activation=activation, stats=stats)
+    out = linear(down_in, w["down_proj"], bias=b("down_proj"), residual=mid, stats=stats)
+    return {"attn_in": attn_in, "o_in": o_in, "mlp_in": mlp_in, "down_in": down_in}, out
+
+
+def prune_decoder_block(weights, hidden, seq_lens, *, forward, stream=None, **cfg):
+    """One step of pruning a model block by block: the dense block's forward pass gives its
+    layers' inputs, every layer is pruned with its input (``prune_block``, H shared by the
+    layers that read the same one), and the hidden states pass through the pruned layers.
+
+    weights, hidden, seq_lens and forward (a dict): as for ``block_forward``; cfg: as for
+    ``prune_layer`` (method, pattern, sparsity, ...).  Returns (results, out): {layer: (W_hat
+    fp32, mask, Stats)} and the pruned block's output, the next block's hidden states.  The
+    pruned weights take part in that pass rounded to the weights' type."""
+    weights = {name: weights[name] for name in FEEDS if name in weights}
+    acts, _ = block_forward(weights, hidden, seq_lens, stream=stream, **forward)
+    results = _pwp.prune_block(weights, acts, FEEDS, stream=stream, **cfg)
+    if stream is None:
+        pruned = {name: results[name][0].to(weights[name].dtype) for name in FEEDS}
+    else:
+        with _pwp._stream_ctx(stream):
+            pruned = {name: results[name][0].to(weights[name].dtype) for name in FEEDS}
+    _, out = block_forward(pruned, hidden, seq_lens, stream=stream, **forward)
+    return results, out

@@ -1,0 +1,89 @@
+// Internal declarations of the decoder block's forward operators (norms, rotated queries
+// and keys, packed attention, projections with their epilogues).
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "pwp_internal.cuh"
+
+namespace pwp {
+
+constexpr int kSiteAttention = 9, kSiteLinear = 10;   // pwp_stats::status_site of these calls
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// Activations of pwp_activation in fp32.  For x far below zero e^-x overflows to infinity
+// and x / inf is -0, the limit of x / (1 + e^-x).
+__device__ __forceinline__ float activate(int act, float x) {
+  switch (act) {
+    case PWP_ACT_RELU: return x != x ? x : fmaxf(x, 0.f);
+    case PWP_ACT_SILU: return __fdividef(x, 1.f + __expf(-x));
+    case PWP_ACT_GELU: return 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
+    case PWP_ACT_GELU_TANH: {
+      const float t = 0.79788456080286536f * (x + 0.044715f * x * x * x);
+      return 0.5f * x * (1.f + tanhf(t));
+    }
+    default: return x;
+  }
+}
+
+// One tile of a packed batch: rows [begin + first, begin + first + per) of the sequence
+// [begin, begin + len).
+struct SeqTile {
+  int begin, len, first;
+};
+
+// Finds tile `t` when every sequence is cut into tiles of `per` rows (whole warp, all lanes
+// get the answer).  The first sequence whose offsets decrease or leave [0, n] and all behind
+// it count as empty, so the sequences taken never overlap; `bad` is set when one is met.
+// Returns false past the last tile.
+__device__ __forceinline__ bool find_seq_tile(const int* __restrict__ cu, int nseq, long long n, int per, int t,
+                                              SeqTile& out, bool& bad) {
+  const int lane = threadIdx.x & 31;
+  for (int s0 = 0; s0 < nseq; s0 += 32) {
+    const int s = s0 + lane;
+    int a = 0, b = 0;
+    if (s < nseq) {
+      a = cu[s];
+      b = cu[s + 1];
+    }
+    const bool ok = a >= 0 && b >= a && (long long)b <= n;
+    const unsigned broken = ~__ballot_sync(0xffffffffu, ok);
+    if (broken) bad = true;
+    const int len = (broken & (0xffffffffu >> (31 - lane))) ? 0 : b - a;
+    const int tiles = (int)(((long long)len + per - 1) / per);
+    int sum = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, t < sum);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      out.begin = __shfl_sync(0xffffffffu, a, l);
+      out.len = __shfl_sync(0xffffffffu, len, l);
+      out.first = (t - __shfl_sync(0xffffffffu, sum - tiles, l)) * per;
+      return true;
+    }
+    if (broken) return false;
+    t -= __shfl_sync(0xffffffffu, sum, 31);
+  }
+  return false;
+}
+
+cudaError_t launch_rms_norm(const void* x, int type, long long rows, int width, long long xs, const void* w, float eps,
+                            void* out, long long os, cudaStream_t s);
+cudaError_t launch_qk_norm_rope(const pwp_rope_args& a, cudaStream_t s);
+cudaError_t launch_attention_simt(const pwp_attention_args& a, cudaStream_t s);
+cudaError_t launch_linear_simt(const pwp_linear_args& a, cudaStream_t s);
+cudaError_t launch_linear_tc(const pwp_linear_args& a, cudaStream_t s, bool* used);
+
+}  // namespace pwp

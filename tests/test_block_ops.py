@@ -1,0 +1,316 @@
+"""The decoder block's forward operators without a GPU: the oracle's formulas against
+independent computations, the frequency scalings, the binding's refusals and marshalling, and
+the C entry points' argument checks."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import post_weight_pruning_b200 as pwp  # noqa: E402
+from oracle import forward as F  # noqa: E402
+from post_weight_pruning_b200 import block as B  # noqa: E402
+
+
+# ------------------------------------------------------------------- the oracle
+
+def test_oracle_attention_matches_the_dense_softmax():
+    rng = np.random.default_rng(0)
+    lens, hq, hk, d = [3, 0, 7, 1], 4, 2, 8
+    n = sum(lens)
+    q, k, v = (rng.normal(size=(n, h, d)) for h in (hq, hk, hk))
+    for causal in (True, False):
+        out, size = F.attention(q, k, v, lens, causal, spread=True)
+        seq = np.repeat(np.arange(len(lens)), lens)
+        sees = seq[:, None] == seq[None]
+        if causal:
+            sees &= np.arange(n)[:, None] >= np.arange(n)[None]
+        for h in range(hq):
+            s = torch.from_numpy(q[:, h] @ k[:, h // 2].T / math.sqrt(d))
+            p = torch.softmax(s.masked_fill(torch.from_numpy(~sees), -math.inf), -1).numpy()
+            np.testing.assert_allclose(out[:, h], p @ v[:, h // 2], rtol=1e-12, atol=1e-14)
+            np.testing.assert_allclose(size[:, h], p @ np.abs(v[:, h // 2]), rtol=1e-12)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_oracle_rotation_depends_on_distances_only(layout):
+    rng = np.random.default_rng(1)
+    q, k = rng.normal(size=(2, 1, 1, 12))
+    f = F.rope_frequencies(8)
+    dots = []
+    for shift in (0, 5, 1000):
+        a, _ = F.qk_norm_rope(q, q, [shift + 7], f, layout=layout)
+        b, _ = F.qk_norm_rope(k, k, [shift + 3], f, layout=layout)
+        assert np.array_equal(a[..., 8:], q[..., 8:])
+        dots.append(float(np.sum(a * b)))
+    assert np.allclose(dots, dots[0], rtol=1e-9)
+
+
+def test_oracle_activations_match_torch():
+    x = torch.linspace(-9, 9, 41, dtype=torch.float64)
+    for name, f in (("relu", torch.relu), ("silu", torch.nn.functional.silu), ("gelu", torch.nn.functional.gelu),
+                    ("gelu_tanh", lambda t: torch.nn.functional.gelu(t, approximate="tanh"))):
+        np.testing.assert_allclose(F.activation(name, x.numpy()), f(x).numpy(), rtol=1e-9, atol=1e-14)
+
+
+# ------------------------------------------------------------------- frequencies
+
+def test_plain_frequencies():
+    f, s = pwp.rope_frequencies(16, base=500.0, device="cpu")
+    assert f.dtype == torch.float64 and s == 1.0
+    np.testing.assert_allclose(f.numpy(), F.rope_frequencies(16, 500.0), rtol=1e-14)
+    assert pwp.rope_frequencies(0, device="cpu")[0].shape == (0,)
+
+
+def test_scaled_frequencies():
+    plain = F.rope_frequencies(128)
+    f, s = pwp.rope_frequencies(128, scaling=dict(type="linear", factor=4.0), device="cpu")
+    np.testing.assert_allclose(f.numpy(), plain / 4, rtol=1e-14)
+    f, _ = pwp.rope_frequencies(128, scaling=dict(type="base", factor=4.0), device="cpu")
+    assert f[0] == 1.0 and math.isclose(float(f[-1]), plain[-1] / 4, rel_tol=1e-12)
+    sc = dict(type="bands", factor=8.0, low_freq_factor=1.0, high_freq_factor=4.0, original_max_positions=8192)
+    f, s = pwp.rope_frequencies(128, scaling=sc, device="cpu")
+    turns = 8192 * plain / (2 * math.pi)
+    np.testing.assert_allclose(f.numpy()[turns >= 4], plain[turns >= 4], rtol=1e-14)
+    np.testing.assert_allclose(f.numpy()[turns <= 1], plain[turns <= 1] / 8, rtol=1e-14)
+    assert np.all(np.diff(f.numpy()) < 0) and s == 1.0
+    sc = dict(type="yarn", factor=16.0, original_max_positions=4096)
+    f, s = pwp.rope_frequencies(128, scaling=sc, device="cpu")
+    assert math.isclose(float(f[0]), 1.0) and math.isclose(float(f[-1]), plain[-1] / 16, rel_tol=1e-12)
+    assert math.isclose(s, 0.1 * math.log(16) + 1)
+
+
+@pytest.mark.parametrize("kw", [dict(rot=3), dict(rot=-2), dict(rot=4, base=0.0), dict(rot=4, scaling=dict(type="x", factor=2)),
+                                dict(rot=4, scaling=dict(type="linear")), dict(rot=2, scaling=dict(type="base", factor=2)),
+                                dict(rot=4, scaling=dict(type="linear", factor=2, other=1)),
+                                dict(rot=4, scaling=dict(type="bands", factor=2, low_freq_factor=4, high_freq_factor=1,
+                                                         original_max_positions=10))])
+def test_frequency_refusals(kw):
+    with pytest.raises(ValueError):
+        pwp.rope_frequencies(**kw, device="cpu")
+
+
+# ------------------------------------------------------------------- refusals and marshalling
+
+class _FakeLib:
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        if not name.startswith("pwp_"):
+            raise AttributeError(name)
+
+        def f(*a):
+            self.calls.append((name, [getattr(x, "_obj", x) for x in a]))
+            return 0
+        return f
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    """The library replaced by a recorder, CPU tensors let through as if they were on a GPU."""
+    f = _FakeLib()
+    monkeypatch.setattr(pwp, "lib", lambda: f)
+    monkeypatch.setattr(pwp, "_stream_ptr", lambda stream=None: ctypes.c_void_p(7))
+
+    def first(t, name, dims):
+        pwp._dtype_code(t)
+        if t.dim() != dims:
+            raise ValueError(name)
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(name)
+    monkeypatch.setattr(B, "_check_first", first)
+    return f
+
+
+def z(*shape, dtype=torch.bfloat16):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def test_operators_refuse_host_tensors():
+    for call in (lambda: pwp.rms_norm(z(2, 4)), lambda: pwp.attention(z(2, 1, 4), z(2, 1, 4), z(2, 1, 4), z(2)),
+                 lambda: pwp.linear(z(2, 4), z(3, 4)), lambda: pwp.gated_linear(z(2, 4), z(3, 4), z(3, 4)),
+                 lambda: pwp.qk_norm_rope(z(2, 1, 4), z(2, 1, 4), z(2), z(2))):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    with pytest.raises(TypeError):
+        pwp.linear(None, z(3, 4))
+
+
+CU = torch.zeros(2, dtype=torch.int32)
+POS = torch.zeros(2, dtype=torch.int64)
+FR = torch.zeros(2, dtype=torch.float64)
+
+
+@pytest.mark.parametrize("call, err", [
+    (lambda: pwp.rms_norm(z(2, 4, dtype=torch.float16)), TypeError),
+    (lambda: pwp.rms_norm(z(2, 4, 1)), ValueError),
+    (lambda: pwp.rms_norm(z(4, 2).T), ValueError),
+    (lambda: pwp.rms_norm(z(2, 4), z(5)), ValueError),
+    (lambda: pwp.rms_norm(z(2, 4), z(4, dtype=torch.float32)), TypeError),
+    (lambda: pwp.rms_norm(z(2, 4), eps=-1.0), ValueError),
+    (lambda: pwp.rms_norm(z(2, 4), eps=math.inf), ValueError),
+    (lambda: pwp.rms_norm(z(2, 4), out=z(1, 4).expand(2, 4)), ValueError),
+    (lambda: pwp.rms_norm(z(2, 4).requires_grad_()), ValueError),
+    (lambda: pwp.rms_norm(z(2, 0)), ValueError),
+    (lambda: pwp.qk_norm_rope(z(2, 3, 4), z(2, 3, 5), POS, FR), ValueError),
+    (lambda: pwp.qk_norm_rope(z(2, 3, 4), z(3, 3, 4), POS, FR), ValueError),
+    (lambda: pwp.qk_norm_rope(z(2, 3, 4), z(2, 3, 4), POS.int(), FR), TypeError),
+    (lambda: pwp.qk_norm_rope(z(2, 3, 4), z(2, 3, 4), POS, FR.float()), TypeError),
+    (lambda: pwp.qk_norm_rope(z(2, 3, 2), z(2, 3, 2), POS, FR), ValueError),
+    (lambda: pwp.qk_norm_rope(z(2, 3, 4), z(2, 3, 4), POS, FR, layout="quarter"), ValueError),
+    (lambda: pwp.qk_norm_rope(z(2, 3, 4), z(2, 3, 4), POS, FR, q_weight=z(3)), ValueError),
+    (lambda: pwp.qk_norm_rope(z(2, 3, 4), z(2, 3, 4), POS, FR, factor=math.nan), ValueError),
+    (lambda: pwp.qk_norm_rope(z(2, 3, 4), z(2, 3, 4), torch.zeros(4, dtype=torch.int64)[::2], FR), ValueError),
+    (lambda: pwp.qk_norm_rope(z(2, 3, 4), z(2, 3, 4), POS, FR, k_out=z(2, 1, 4).expand(2, 3, 4)), ValueError),
+    (lambda: pwp.attention(z(2, 3, 4), z(2, 2, 4), z(2, 2, 4), CU), ValueError),
+    (lambda: pwp.attention(z(2, 2, 4), z(2, 2, 4), z(2, 1, 4), CU), ValueError),
+    (lambda: pwp.attention(z(2, 2, 4), z(2, 2, 4), z(2, 2, 4), CU.long()), TypeError),
+    (lambda: pwp.attention(z(2, 2, 4), z(2, 2, 4), z(2, 2, 4), CU[:0]), ValueError),
+    (lambda: pwp.attention(z(2, 2, 4), z(2, 2, 4), z(2, 2, 4, dtype=torch.float32), CU), TypeError),
+    (lambda: pwp.attention(z(2, 2, 257), z(2, 2, 257), z(2, 2, 257), CU), ValueError),
+    (lambda: pwp.attention(z(2, 2, 4), z(2, 2, 4), z(2, 2, 4), CU, scale=math.inf), ValueError),
+    (lambda: pwp.attention(z(2, 2, 4), z(2, 2, 4), z(2, 2, 4), CU, stats=z(8)), ValueError),
+    (lambda: pwp.attention(z(2, 2, 4), z(2, 2, 4), z(2, 2, 4), CU, out=z(2, 2, 4, dtype=torch.float32)), TypeError),
+    (lambda: pwp.linear(z(2, 4), z(3, 5)), ValueError),
+    (lambda: pwp.linear(z(2, 4), z(3, 4, dtype=torch.float32)), TypeError),
+    (lambda: pwp.linear(z(2, 4), z(4, 3).T), ValueError),
+    (lambda: pwp.linear(z(2, 4), z(3, 4), bias=z(4)), ValueError),
+    (lambda: pwp.linear(z(2, 4), z(3, 4), residual=z(3, 3)), ValueError),
+    (lambda: pwp.linear(z(2, 4), z(3, 4), activation="tanh"), ValueError),
+    (lambda: pwp.linear(z(2, 4), z(3, 4), out=z(2, 4)), ValueError),
+    (lambda: pwp.linear(z(2, 4), z(3, 4), out=z(1, 3).expand(2, 3)), ValueError),
+    (lambda: pwp.linear(z(2, 0), z(3, 0)), ValueError),
+    (lambda: pwp.linear(z(2, 4), z(3, 4).requires_grad_()), ValueError),
+    (lambda: pwp.gated_linear(z(2, 4), z(3, 4), z(2, 4)), ValueError),
+    (lambda: pwp.gated_linear(z(2, 4), z(3, 4), z(3, 4), bias_up=z(2)), ValueError),
+])
+def test_refusals(fake, call, err):
+    with pytest.raises(err):
+        call()
+    assert not fake.calls
+
+
+def test_no_grad_lets_parameters_through(fake):
+    with torch.no_grad():
+        pwp.linear(z(2, 4), z(3, 4).requires_grad_())
+    assert len(fake.calls) == 1
+
+
+def test_calls_without_rows_launch_nothing(fake):
+    assert pwp.rms_norm(z(0, 4)).shape == (0, 4)
+    assert pwp.linear(z(0, 4), z(3, 4)).shape == (0, 3)
+    assert pwp.attention(z(0, 2, 4), z(0, 2, 4), z(0, 2, 4), CU).shape == (0, 2, 4)
+    assert pwp.attention(z(2, 2, 4), z(2, 2, 4), z(2, 2, 4), CU[:1]).shape == (2, 2, 4)
+    q, k = pwp.qk_norm_rope(z(0, 2, 4), z(0, 1, 4), POS[:0], FR)
+    assert q.shape == (0, 2, 4) and k.shape == (0, 1, 4)
+    assert not fake.calls
+
+
+def test_marshalling(fake):
+    packed = z(5, 40)
+    q, k, v = packed[:, :16].view(5, 2, 8), packed[:, 16:24].view(5, 1, 8), packed[:, 32:].view(5, 1, 8)
+    cu = torch.tensor([0, 2, 5], dtype=torch.int32)
+    out = pwp.attention(q, k, v, cu, causal=False)
+    a = fake.calls[-1][1][0]
+    assert fake.calls[-1][0] == "pwp_attention"
+    assert (a.q, a.k, a.v, a.out, a.cu_seqlens) == tuple(t.data_ptr() for t in (q, k, v, out, cu))
+    assert list(a.q_stride) == [40, 8] and list(a.v_stride) == [40, 8] and list(a.out_stride) == [16, 8]
+    assert (a.n, a.nseq, a.type, a.hq, a.hk, a.d, a.causal) == (5, 2, pwp.BF16, 2, 1, 8, 0)
+    assert a.stats is None and math.isclose(a.scale, 8 ** -0.5, rel_tol=1e-6)
+
+    pos = torch.arange(5)
+    fr = torch.ones(2, dtype=torch.float64)
+    w = z(8)
+    qo, ko = pwp.qk_norm_rope(q, k, pos, fr, k_weight=w, layout="interleaved", factor=1.5, q_out=q)
+    a = fake.calls[-1][1][0]
+    assert qo is q and a.q_out == q.data_ptr() and a.k_out == ko.data_ptr() and ko.shape == (5, 1, 8)
+    assert (a.rot, a.layout, a.q_weight, a.k_weight, a.factor) == (4, 1, None, w.data_ptr(), 1.5)
+
+    x, wg, wu, b, r = z(3, 4), z(6, 4), z(6, 4), z(6), z(3, 6)
+    pwp.linear(x, wg, bias=b, activation="gelu", residual=r, out=r)
+    a = fake.calls[-1][1][0]
+    assert (a.w_up, a.bias, a.residual, a.out) == (None, b.data_ptr(), r.data_ptr(), r.data_ptr())
+    assert (a.rows, a.k, a.n, a.activation, a.out_stride) == (3, 4, 6, 3, 6)
+    pwp.gated_linear(x, wg, wu, bias_up=b)
+    a = fake.calls[-1][1][0]
+    assert (a.w, a.w_up, a.bias, a.bias_up, a.activation) == (wg.data_ptr(), wu.data_ptr(), None, b.data_ptr(), 2)
+    pwp.rms_norm(x, eps=0.5)
+    assert fake.calls[-1][0] == "pwp_rms_norm" and fake.calls[-1][1][6] == 0.5
+
+
+def test_block_forward_refusals(fake):
+    w = {p: z(8, 8) for p in B.FEEDS}
+    with pytest.raises(ValueError, match="missing"):
+        pwp.block_forward({}, z(4, 8), [4], heads=1)
+    with pytest.raises(ValueError, match="seq_lens"):
+        pwp.block_forward(w, z(4, 8), [3], heads=1)
+    with pytest.raises(ValueError, match="seq_lens"):
+        pwp.block_forward(w, z(4, 8), [5, -1], heads=1)
+    with pytest.raises(ValueError, match="heads"):
+        pwp.block_forward(w, z(4, 8), [4], heads=3)
+    with pytest.raises(ValueError, match="norms"):
+        pwp.block_forward(w, z(4, 8), [4], heads=1, norms={"x": z(8)})
+    with pytest.raises(ValueError, match="biases"):
+        pwp.block_forward(w, z(4, 8), [4], heads=1, biases={"x": z(8)})
+
+
+def test_struct_sizes_match_the_header(tmp_path):
+    import os
+    import shutil
+    import subprocess
+    if shutil.which("gcc") is None:
+        pytest.skip("no C compiler")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "s.c"
+    src.write_text('#include <stdio.h>\n#include "pwp.h"\nint main(void) { printf("%zu %zu %zu\\n", sizeof(pwp_rope_args), '
+                   'sizeof(pwp_attention_args), sizeof(pwp_linear_args)); return 0; }\n')
+    exe = tmp_path / "s"
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", os.path.join(root, "include"), str(src), "-o", str(exe)],
+                   check=True)
+    got = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()
+    assert [int(x) for x in got] == [ctypes.sizeof(t) for t in (B.RopeArgs, B.AttentionArgs, B.LinearArgs)]
+
+
+def test_c_entry_points_check_their_arguments():
+    L = pwp.lib()
+    p = ctypes.c_void_p(256)   # never dereferenced: every call below is refused first
+
+    def rms(rows=1, width=4, eps=1e-5, x=p, os=4, type=0):
+        return L.pwp_rms_norm(x, type, rows, width, 4, None, eps, p, os, None)
+    assert rms(rows=-1) == rms(width=0) == rms(eps=-1.0) == rms(eps=math.nan) == rms(x=None) == rms(type=2) == 1
+    assert rms(rows=2, os=3) == 1 and rms(rows=0) == 0
+
+    def att(**kw):
+        a = B.AttentionArgs(q=256, k=256, v=256, out=256, cu_seqlens=256, n=4, nseq=1, type=0, hq=2, hk=1, d=8,
+                            causal=1, scale=1.0)
+        for key, val in kw.items():
+            setattr(a, key, val)
+        return L.pwp_attention(ctypes.byref(a), None)
+    for kw in (dict(hq=3, hk=2), dict(hk=0), dict(d=257), dict(d=0), dict(n=-1), dict(n=1 << 31), dict(nseq=-1),
+               dict(scale=math.inf), dict(q=None), dict(cu_seqlens=None), dict(type=3)):
+        assert att(**kw) == 1, kw
+    assert att(n=0) == att(nseq=0) == 0 and L.pwp_attention(None, None) == 1
+
+    def lin(**kw):
+        a = B.LinearArgs(x=256, w=256, out=256, rows=2, k=4, n=4, x_stride=4, w_stride=4, out_stride=4)
+        for key, val in kw.items():
+            setattr(a, key, val)
+        return L.pwp_linear(ctypes.byref(a), None)
+    for kw in (dict(rows=-1), dict(k=0), dict(n=0), dict(k=1 << 24), dict(activation=5), dict(activation=-1), dict(x=None),
+               dict(bias_up=256), dict(out_stride=3), dict(type=9)):
+        assert lin(**kw) == 1, kw
+    assert lin(rows=0) == 0 and L.pwp_linear(None, None) == 1
+
+    def rope(**kw):
+        a = B.RopeArgs(q=256, k=256, q_out=256, k_out=256, positions=256, freqs=256, n=1, hq=1, hk=1, d=8, rot=8,
+                       eps=1e-5, factor=1.0)
+        for key, val in kw.items():
+            setattr(a, key, val)
+        return L.pwp_qk_norm_rope(ctypes.byref(a), None)
+    for kw in (dict(rot=7), dict(rot=10), dict(d=0), dict(d=1025), dict(layout=2), dict(hq=-1), dict(n=-1), dict(q=None),
+               dict(freqs=None), dict(eps=-1.0), dict(factor=math.inf)):
+        assert rope(**kw) == 1, kw
+    assert rope(n=0) == 0 and L.pwp_qk_norm_rope(None, None) == 1

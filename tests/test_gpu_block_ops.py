@@ -1,0 +1,473 @@
+"""GPU parity of the decoder block's forward operators against the fp64 oracle.
+
+Tolerances, elementwise and derived from the arithmetic (u = half a step of the output type:
+2^-8 for bf16, 2^-24 for fp32; g = 2^-23, one fp32 step, which bounds an addition rounded
+either way):
+  rms_norm       |y| (u + 2^-8 * 0): the fp32 sum over b terms of one sign is off by less than
+                 (b / 32 + 16) g (a thread's chain, then a tree), halved by the root, and four
+                 more operations follow: u + (b / 64 + 16) g
+  qk_norm_rope   the same for the norm; the turn adds |a c| and |b s| each off by 4 g, so
+                 u |y| + ((d / 64 + 16) g) (|a c| + |b s|), bounded by factor * (|a| + |b|)
+  linear         products of bf16 are exact in fp32; a sum of k terms in chains of at most
+                 k / 16 + 32 additions (16 terms of one instruction, then one accumulator):
+                 (k / 16 + 32) g S, S = sum |x w| + |bias|; fp32 tensors: every product is also
+                 rounded and the chain is k long: (k + 4) g S.  Activations have slope at most
+                 1.13 and are themselves good to 8 g; u |y| and the residual's addition follow.
+  attention      probabilities of the tensor-core kernel are rounded to bf16 (2^-8 of each, so
+                 2^-8 sum p|v|), the exponential is good to 2^-12 of itself, and a score is off
+                 by (d / 16 + 40) g scale sum |q k|, which is a relative error of p and of the
+                 sum; output rounding u |o|.
+"""
+import math
+
+import numpy as np
+import pytest
+
+from oracle import forward as F
+
+pytestmark = pytest.mark.gpu
+G = 2.0 ** -23
+
+
+def _torch():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return torch
+
+
+def _pwp():
+    import post_weight_pruning_b200 as pwp
+    return pwp
+
+
+def U(dtype):
+    return 2.0 ** -8 if "bf" in str(dtype) else 2.0 ** -24
+
+
+def dt(name):
+    torch = _torch()
+    return torch.bfloat16 if name == "bf16" else torch.float32
+
+
+def rnd(shape, dtype, seed, scale=1.0):
+    torch = _torch()
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(dt(dtype)).cuda()
+
+
+def np64(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def close(got, want, tol, what=""):
+    got = np64(got)
+    assert got.shape == want.shape, (got.shape, want.shape)
+    assert np.array_equal(np.isnan(got), np.isnan(want)), what
+    bad = np.abs(got - want) > tol
+    assert not bad.any(), (what, int(bad.sum()), np.argwhere(bad)[:4].tolist(),
+                           float(np.nanmax(np.abs(got - want) / np.maximum(tol, 1e-300))))
+
+
+# ------------------------------------------------------------------- rms_norm
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,b", [(1, 1), (1, 4096), (3, 7), (5, 130), (2, 1000), (300, 256), (7, 8192), (2, 11008),
+                                 (3, 30001), (9, 72)])
+def test_rms_norm(n, b, dtype):
+    pwp = _pwp()
+    x, w = rnd((n, b), dtype, 1, 3.0), rnd((b,), dtype, 2)
+    for weight in (w, None):
+        y = pwp.rms_norm(x, weight)
+        want = F.rms_norm(np64(x), np64(weight))
+        close(y, want, np.abs(want) * (U(x.dtype) + (b / 64 + 16) * G) + 1e-37)
+
+
+def test_rms_norm_strides_in_place_and_zero_rows():
+    torch, pwp = _torch(), _pwp()
+    big = rnd((6, 200), "bf16", 3)
+    big[2] = 0
+    for cut in (slice(0, 96), slice(8, 136), slice(3, 50)):
+        keep = big.clone()
+        x = keep[:, cut]
+        want = F.rms_norm(np64(x))
+        y = pwp.rms_norm(x, out=x)
+        assert y is x
+        close(y, want, np.abs(want) * (U(x.dtype) + 32 * G))
+        outside = torch.ones(200, dtype=torch.bool)
+        outside[cut] = False
+        assert torch.equal(keep[:, outside.cuda()], big[:, outside.cuda()])
+    assert torch.equal(pwp.rms_norm(big)[2], torch.zeros_like(big[2]))
+
+
+# ------------------------------------------------------------------- qk_norm_rope
+
+def rope_tol(q, freqs, weight, eps, layout, factor, want, u, d):
+    y = np64(q) if weight is None else F.rms_norm(np64(q), np64(weight), eps)
+    mag = np.abs(y)
+    rot = 2 * len(freqs)
+    for i in range(rot // 2):
+        a, b = (i, i + rot // 2) if layout == "half" else (2 * i, 2 * i + 1)
+        mag[..., a] = mag[..., b] = factor * (mag[..., a] + mag[..., b])
+    return u * np.abs(want) + (d / 64 + 16) * G * mag + 1e-37
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,hq,hk,d,rot,layout,norm,first", [
+    (1, 1, 1, 2, 2, "half", False, 0),
+    (5, 4, 2, 128, 128, "half", True, 0),
+    (5, 4, 2, 128, 128, "interleaved", False, 1000000),
+    (33, 8, 1, 64, 32, "half", True, 5),
+    (9, 3, 3, 80, 80, "half", False, 100000),
+    (9, 7, 1, 96, 48, "interleaved", True, 77),
+    (4, 2, 0, 128, 64, "half", True, 3),
+    (3, 2, 1, 33, 10, "half", True, 9),
+    (3, 2, 1, 40, 12, "interleaved", True, 9),
+    (2, 1, 1, 256, 256, "half", True, 11),
+    (2, 2, 1, 128, 0, "half", True, 11),
+    (70, 32, 8, 128, 64, "interleaved", True, 900000),
+])
+def test_qk_norm_rope(n, hq, hk, d, rot, layout, norm, first, dtype):
+    torch, pwp = _torch(), _pwp()
+    packed = rnd((n, (hq + 2 * hk) * d), dtype, 5)
+    q, k = packed[:, :hq * d].view(n, hq, d), packed[:, hq * d:(hq + hk) * d].view(n, hk, d)
+    qw, kw = (rnd((d,), dtype, 6), rnd((d,), dtype, 7)) if norm else (None, None)
+    pos = first + 3 * torch.arange(n, device="cuda")
+    f, _ = pwp.rope_frequencies(rot, base=1e4)
+    factor = 1.25
+    want = F.qk_norm_rope(np64(q), np64(k), pos.cpu().numpy(), np64(f), np64(qw), np64(kw), 1e-5, layout, factor)
+    got = pwp.qk_norm_rope(q, k, pos, f, q_weight=qw, k_weight=kw, layout=layout, factor=factor)
+    for x, w, y, e in ((q, qw, got[0], want[0]), (k, kw, got[1], want[1])):
+        close(y, e, rope_tol(x, np64(f), w, 1e-5, layout, factor, e, U(x.dtype), d))
+    # in place, on slices of the packed projection: bit for bit the same, v untouched
+    before = packed.clone()
+    q2, k2 = pwp.qk_norm_rope(q, k, pos, f, q_weight=qw, k_weight=kw, layout=layout, factor=factor, q_out=q, k_out=k)
+    assert q2 is q and torch.equal(q, got[0]) and torch.equal(k, got[1])
+    assert torch.equal(packed[:, (hq + hk) * d:], before[:, (hq + hk) * d:])
+
+
+def test_qk_norm_rope_head_major_and_negative_positions():
+    torch, pwp = _torch(), _pwp()
+    n, h, d = 6, 4, 64
+    q = rnd((h, n, d), "bf16", 8).transpose(0, 1)
+    pos = torch.tensor([-5, 0, 3, 2 ** 40 + 1, 7, 7], device="cuda")
+    f, _ = pwp.rope_frequencies(d)
+    qo, ko = pwp.qk_norm_rope(q, q, pos, f)
+    # at 2^40 the double angle itself is off by up to 2^-52 of 2^40 radians
+    want = F.qk_norm_rope(np64(q), np64(q), pos.cpu().numpy(), np64(f))[0]
+    close(qo, want, rope_tol(q, np64(f), None, 0, "half", 1.0, want, U(q.dtype), d) + 2.0 ** -10)
+    assert torch.equal(qo, ko)
+
+
+# ------------------------------------------------------------------- attention
+
+def att_case(lens, hq, hk, d, dtype, seed, extra=0, qscale=1.5):
+    torch = _torch()
+    n = sum(lens) + extra
+    q, k, v = rnd((n, hq, d), dtype, seed, qscale), rnd((n, hk, d), dtype, seed + 1), rnd((n, hk, d), dtype, seed + 2)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    return q, k, v, cu
+
+
+def att_tol(q, k, lens, hq, hk, d, want, size, dtype, scale=None):
+    scale = d ** -0.5 if scale is None else scale
+    s = scale * float(np.max(np.linalg.norm(np64(q), axis=-1)) * np.max(np.linalg.norm(np64(k), axis=-1)))
+    if dtype == "fp32":
+        rel = (d + 8) * G * s + 64 * G
+        return U(dtype) * np.abs(want) + (2 * rel + (max(lens) + 8) * G) * size + 1e-30
+    rel = (d / 16 + 40) * G * s + 2.0 ** -12
+    return U(dtype) * np.abs(want) + (2.0 ** -8 + 2 * rel + (max(lens) / 16 + 40) * G) * size + 1e-30
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,hq,hk,d,dtype", [
+    ([1], 1, 1, 64, "bf16"),
+    ([1, 0, 2, 0, 0, 3], 4, 2, 128, "bf16"),
+    ([127, 128, 129], 2, 2, 128, "bf16"),
+    ([300], 4, 1, 128, "bf16"),
+    ([5, 260, 64], 8, 2, 64, "bf16"),
+    ([33, 140], 5, 1, 80, "bf16"),          # a group that does not divide a tile
+    ([200], 7, 1, 96, "bf16"),
+    ([70], 3, 1, 128, "bf16"),
+    ([257], 40, 8, 128, "bf16"),
+    ([19, 300], 16, 1, 128, "bf16"),
+    ([130], 129, 1, 64, "bf16"),            # more heads in a group than a tile has rows
+    ([40, 9], 2, 1, 20, "bf16"),            # head size the copies cannot take
+    ([50], 2, 1, 136, "bf16"),
+    ([70, 1, 33], 4, 2, 128, "fp32"),
+    ([100], 2, 1, 33, "fp32"),
+    ([65], 1, 1, 256, "fp32"),
+])
+def test_attention(lens, hq, hk, d, dtype, causal):
+    pwp = _pwp()
+    q, k, v, cu = att_case(lens, hq, hk, d, dtype, 11)
+    want, size = F.attention(np64(q), np64(k), np64(v), lens, causal, spread=True)
+    st = pwp.new_stats()
+    got = pwp.attention(q, k, v, cu, causal=causal, stats=st)
+    assert pwp.read_stats(st).status == 0
+    close(got, want, att_tol(q, k, lens, hq, hk, d, want, size, dtype))
+
+
+def test_attention_strided_scaled_and_rows_left_alone():
+    """q, k, v as slices of one packed buffer and head-major; an output with room around it; a
+    scale of one's own; rows before the first and behind the last sequence keep their content."""
+    torch, pwp = _torch(), _pwp()
+    lens, hq, hk, d, extra = [30, 170], 4, 2, 128, 9
+    n = sum(lens) + 2 * extra
+    packed = rnd((n, (hq + 2 * hk) * d), "bf16", 21)
+    q, k, v = (x.view(n, -1, d) for x in packed.split([hq * d, hk * d, hk * d], dim=1))
+    v = v.transpose(0, 1).contiguous().transpose(0, 1)
+    packed[:extra] = float("nan")
+    packed[n - extra:] = float("inf")
+    v[:extra] = float("inf")
+    v[n - extra:] = float("nan")
+    cu = (extra + torch.tensor([0, 30, 200])).to(torch.int32).cuda()
+    room = torch.full((n, hq + 3, d + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = room[:, 1:hq + 1, :d]
+    s = slice(extra, n - extra)
+    got = pwp.attention(q, k, v, cu, scale=0.05, out=out)
+    want, size = F.attention(np64(q[s]), np64(k[s]), np64(v[s]), lens, True, 0.05, spread=True)
+    close(got[s], want, att_tol(q[s], k[s], lens, hq, hk, d, want, size, "bf16", 0.05))
+    room[s, 1:hq + 1, :d] = 7.0
+    assert bool((room == 7.0).all())
+
+
+@pytest.mark.parametrize("hq,hk,dtype", [(2, 2, "bf16"), (8, 2, "bf16"), (2, 1, "fp32")])
+def test_attention_later_tokens_never_reach_a_query(hq, hk, dtype):
+    """Causal: NaN and infinities in the values and keys of later tokens leave earlier queries
+    as they are, bit for bit; the queries that see them get them."""
+    torch, pwp = _torch(), _pwp()
+    lens, d, at = [300], 128, 140
+    q, k, v, cu = att_case(lens, hq, hk, d, dtype, 31)
+    clean = pwp.attention(q, k, v, cu)
+    v2, k2 = v.clone(), k.clone()
+    v2[at, :, 3] = float("nan")
+    v2[at + 1, :, 5] = float("inf")
+    v2[at + 5, :, 5] = -float("inf")
+    got = pwp.attention(q, k, v2, cu)
+    assert torch.equal(got[:at], clean[:at])
+    assert bool(got[at:, :, 3].isnan().all())
+    assert bool((got[at + 1:at + 5, :, 5] == float("inf")).all()) and bool(got[at + 5:, :, 5].isnan().all())
+    others = [c for c in range(d) if c not in (3, 5)]
+    assert torch.equal(got[:, :, others], clean[:, :, others])
+    k2[at] = float("nan")
+    got = pwp.attention(q, k2, v, cu)
+    assert torch.equal(got[:at], clean[:at]) and bool(got[at:].isnan().all())
+
+
+def test_attention_bad_offsets_are_reported():
+    torch, pwp = _torch(), _pwp()
+    q, k, v, _ = att_case([100], 2, 1, 64, "bf16", 41)
+    good = pwp.attention(q, k, v, torch.tensor([0, 40, 100], dtype=torch.int32, device="cuda"))
+    for offsets in ([0, 40, 30, 100], [0, 40, 101], [0, 40, -5, 100], [0, 40, 2 ** 31 - 1]):
+        out = torch.full_like(q, 7.0)
+        st = pwp.new_stats()
+        pwp.attention(q, k, v, torch.tensor(offsets, dtype=torch.int32, device="cuda"), out=out, stats=st)
+        assert pwp.read_stats(st).status == 1
+        assert torch.equal(out[:40], good[:40]) and bool((out[40:] == 7.0).all())
+
+
+def test_attention_many_sequences_and_large_scores():
+    torch, pwp = _torch(), _pwp()
+    rng = np.random.default_rng(3)
+    lens = rng.integers(0, 9, size=150).tolist()
+    q, k, v, cu = att_case(lens, 2, 1, 64, "bf16", 51, qscale=40.0)     # nearly one-hot rows
+    want, size = F.attention(np64(q), np64(k), np64(v), lens, True, spread=True)
+    close(pwp.attention(q, k, v, cu), want, att_tol(q, k, lens, 2, 1, 64, want, size, "bf16"))
+    # scores that rise along the keys: the running maximum moves at every tile
+    n = 520
+    q = torch.zeros(n, 1, 64, dtype=torch.bfloat16, device="cuda")
+    q[:, 0, 0] = 8.0
+    k = torch.zeros_like(q)
+    k[:, 0, 0] = torch.arange(n, device="cuda") * 0.25
+    v = rnd((n, 1, 64), "bf16", 52)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    want, size = F.attention(np64(q), np64(k), np64(v), [n], True, 1.0, spread=True)
+    close(pwp.attention(q, k, v, cu, scale=1.0), want, att_tol(q, k, [n], 1, 1, 64, want, size, "bf16", 1.0))
+
+
+# ------------------------------------------------------------------- linear, gated_linear
+
+def lin_tol(x, w, bias, act, pre, y, res, dtype, slope=1.13):
+    k = x.shape[1]
+    s = np.abs(np64(x)) @ np.abs(np64(w)).T + (0 if bias is None else np.abs(np64(bias)))
+    e = ((k / 16 + 32) if dtype == "bf16" else (k + 4)) * G * s
+    return slope * e + 8 * G * np.abs(pre)
+
+
+ACTS = ["none", "relu", "silu", "gelu", "gelu_tanh"]
+
+
+@pytest.mark.parametrize("rows,k,n,dtype", [
+    (1, 1, 1, "bf16"), (1, 64, 128, "bf16"), (1, 4096, 520, "bf16"), (3, 200, 24, "bf16"), (17, 1000, 136, "bf16"),
+    (64, 256, 256, "bf16"), (129, 72, 1000, "bf16"), (300, 520, 264, "bf16"), (256, 128, 512, "bf16"),
+    (700, 640, 1032, "bf16"), (33, 100, 77, "bf16"), (5, 33, 40, "bf16"), (260, 8, 8, "bf16"), (1100, 512, 1536, "bf16"),
+    (1, 5, 3, "fp32"), (70, 130, 65, "fp32"), (200, 64, 128, "fp32"),
+])
+def test_linear_and_gated(rows, k, n, dtype):
+    pwp = _pwp()
+    x, w, wu = rnd((rows, k), dtype, 61), rnd((n, k), dtype, 62, 0.05), rnd((n, k), dtype, 63, 0.05)
+    b, bu, r = rnd((n,), dtype, 64), rnd((n,), dtype, 65), rnd((rows, n), dtype, 66)
+    u = U(dtype)
+    st = pwp.new_stats()
+    for i, act in enumerate(ACTS):
+        bias, res = (b if i != 1 else None), (r if i % 2 == 0 else None)
+        pre = F.linear(np64(x), np64(w), np64(bias))
+        want = F.linear(np64(x), np64(w), np64(bias), act, np64(res))
+        tol = lin_tol(x, w, bias, act, pre, want, res, dtype)
+        if res is not None:
+            tol = tol + G * np.abs(np64(res))
+        close(pwp.linear(x, w, bias=bias, activation=act, residual=res, stats=st), want, tol + u * np.abs(want) + 1e-37,
+              act)
+        up = F.linear(np64(x), np64(wu), np64(bu))
+        want = F.gated_linear(np64(x), np64(w), np64(wu), np64(bias), np64(bu), act)
+        eg = lin_tol(x, w, bias, act, pre, want, None, dtype)
+        eu = lin_tol(x, wu, bu, "none", up, want, None, dtype, 1.0)
+        g = F.activation(act, pre)
+        tol = eg * np.abs(up) + eu * np.abs(g) + eg * eu + 2 * G * np.abs(want)
+        close(pwp.gated_linear(x, w, wu, bias_gate=bias, bias_up=bu, activation=act, stats=st), want,
+              tol + u * np.abs(want) + 1e-37, "gated " + act)
+    assert pwp.read_stats(st).status == 0
+
+
+@pytest.mark.parametrize("rows", [3, 300, 1100])
+def test_linear_strides_and_residual_in_place(rows):
+    torch, pwp = _torch(), _pwp()
+    k, n = 192, 264
+    for off, pad in ((8, 16), (3, 5)):       # what the copies can take, and what they cannot
+        xb, rb = rnd((rows, k + off + pad), "bf16", 71), rnd((rows, n + off + pad), "bf16", 72)
+        x, r, w = xb[:, off:off + k], rb[:, off:off + n], rnd((n, k), "bf16", 73, 0.05)
+        want = F.linear(np64(x), np64(w), None, "silu", np64(r))
+        pre = F.linear(np64(x), np64(w))
+        tol = lin_tol(x, w, None, "silu", pre, want, r, "bf16") + G * np.abs(np64(r)) + 2.0 ** -8 * np.abs(want)
+        before = rb.clone()
+        apart = pwp.linear(x, w, activation="silu", residual=r)
+        close(apart, want, tol)
+        assert pwp.linear(x, w, activation="silu", residual=r, out=r) is r
+        assert torch.equal(r, apart)
+        assert torch.equal(rb[:, :off], before[:, :off]) and torch.equal(rb[:, off + n:], before[:, off + n:])
+
+
+def test_linear_non_finite_rows_stay_theirs():
+    torch, pwp = _torch(), _pwp()
+    for rows in (40, 600):
+        x, w = rnd((rows, 256), "bf16", 81), rnd((304, 256), "bf16", 82)
+        clean = pwp.linear(x, w)
+        x2 = x.clone()
+        x2[7, 3] = float("nan")
+        got = pwp.linear(x2, w)
+        assert bool(got[7].isnan().all())
+        got[7] = clean[7]
+        assert torch.equal(got, clean)
+
+
+def test_gated_extremes():
+    """Far in the tails silu is x or 0 (and never NaN for finite sums)."""
+    torch, pwp = _torch(), _pwp()
+    x = torch.tensor([[1.0, 0.0], [0.0, 1.0]], dtype=torch.bfloat16, device="cuda").repeat(1, 32)
+    w = torch.full((8, 64), 100.0, dtype=torch.bfloat16, device="cuda")
+    w[::2] = -100.0
+    up = torch.full((8, 64), 0.5, dtype=torch.bfloat16, device="cuda")
+    y = pwp.gated_linear(x, w, up)
+    assert torch.equal(y[:, 1::2], torch.full_like(y[:, 1::2], 3200.0 * 16.0))
+    assert bool((y[:, ::2] == 0).all())
+
+
+# ------------------------------------------------------------------- streams, graphs, timeouts
+
+def _ops(pwp, torch):
+    """Every operator once over sizes that take each kernel; returns the outputs."""
+    q, k, v, cu = att_case([5, 300, 70], 8, 2, 128, "bf16", 91)
+    f, _ = pwp.rope_frequencies(128)
+    pos = torch.arange(q.shape[0], device="cuda")
+    outs = []
+    xs = [rnd((r, 512), "bf16", 92 + r) for r in (2, 70, 1500)]
+    w, wu = rnd((1040, 512), "bf16", 93, 0.05), rnd((1040, 512), "bf16", 94, 0.05)
+    torch.cuda.synchronize()
+
+    def run(stream=None):
+        outs.clear()
+        qr, kr = pwp.qk_norm_rope(q, k, pos, f, stream=stream)
+        outs.extend([qr, kr, pwp.attention(qr, kr, v, cu, stream=stream)])
+        for x in xs:
+            y = pwp.rms_norm(x, stream=stream)
+            outs.extend([y, pwp.linear(y, w, stream=stream), pwp.gated_linear(y, w, wu, stream=stream)])
+        return list(outs)
+    return run
+
+
+def test_operators_on_a_stream_of_their_own_and_in_a_graph():
+    torch, pwp = _torch(), _pwp()
+    run = _ops(pwp, torch)
+    want = run()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = run(s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            kept = run()
+    for _ in range(2):
+        for t in kept:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(kept, want))
+
+
+# ------------------------------------------------------------------- the block
+
+def _block(dtype, heads, kv, width, ff, n, seed=111):
+    d = width // heads
+    w = {p: rnd(s, dtype, seed + i, 1.5 / math.sqrt(s[1])) for i, (p, s) in enumerate(
+        {"q_proj": (heads * d, width), "k_proj": (kv * d, width), "v_proj": (kv * d, width), "o_proj": (width, heads * d),
+         "gate_proj": (ff, width), "up_proj": (ff, width), "down_proj": (width, ff)}.items())}
+    norms = {"attn": 1 + rnd((width,), dtype, seed + 10, 0.1), "mlp": 1 + rnd((width,), dtype, seed + 11, 0.1),
+             "q": 1 + rnd((d,), dtype, seed + 12, 0.1), "k": 1 + rnd((d,), dtype, seed + 13, 0.1)}
+    return w, rnd((n, width), dtype, seed + 14), norms
+
+
+@pytest.mark.parametrize("dtype,tol", [("fp32", 1e-5), ("bf16", 0.03)])
+def test_block_forward_matches_the_oracle(dtype, tol):
+    """All operators in a row, as a block uses them.  bf16: a dozen roundings of 2^-8 in a row,
+    each input's of random sign -- the relative Frobenius error of every activation stays
+    within 8 * 2^-8; fp32: sums of a few hundred terms, 1e-5."""
+    pwp = _pwp()
+    lens = [37, 1, 150]
+    w, x, norms = _block(dtype, 8, 2, 512, 1000, sum(lens))
+    f, _ = pwp.rope_frequencies(64)
+    st = pwp.new_stats()
+    acts, out = pwp.block_forward(w, x, lens, heads=8, kv_heads=2, freqs=f, norms=norms, stats=st)
+    assert pwp.read_stats(st).status == 0
+    want, wout = F.block_forward({p: np64(t) for p, t in w.items()}, np64(x), lens, 8, 2, np64(f),
+                                 norms={p: np64(t) for p, t in norms.items()})
+    assert set(acts) == {"attn_in", "o_in", "mlp_in", "down_in"}
+    for name, got, e in [(m, acts[m], want[m]) for m in acts] + [("out", out, wout)]:
+        rel = np.linalg.norm(np64(got) - e) / np.linalg.norm(e)
+        assert rel <= tol, (name, rel)
+
+
+def test_prune_decoder_block():
+    """The block's layers are pruned with the activations of the dense pass, exactly as
+    prune_block does with them, and the hidden states pass through the pruned layers."""
+    torch, pwp = _torch(), _pwp()
+    lens = [200, 312]
+    w, x, norms = _block("bf16", 4, 2, 256, 640, sum(lens), 131)
+    f, _ = pwp.rope_frequencies(64)
+    fwd = dict(heads=4, kv_heads=2, freqs=f, norms=norms)
+    res, out = pwp.prune_decoder_block(w, x, lens, forward=fwd, method="thanos", pattern="nm", nm=(2, 4), block=64)
+    acts, dense = pwp.block_forward(w, x, lens, **fwd)
+    want = pwp.prune_block(w, acts, pwp.FEEDS, method="thanos", pattern="nm", nm=(2, 4), block=64)
+    for layer in w:
+        assert torch.equal(res[layer][0], want[layer][0]) and torch.equal(res[layer][1], want[layer][1])
+        assert res[layer][2].pruned == w[layer].numel() // 2
+    _, again = pwp.block_forward({p: t[0].bfloat16() for p, t in res.items()}, x, lens, **fwd)
+    assert torch.equal(out, again) and not torch.equal(out, dense)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    res2, out2 = pwp.prune_decoder_block(w, x, lens, forward=fwd, stream=s, method="thanos", pattern="nm", nm=(2, 4),
+                                         block=64)
+    s.synchronize()
+    assert torch.equal(out2, out) and all(torch.equal(res2[p][0], res[p][0]) for p in w)
