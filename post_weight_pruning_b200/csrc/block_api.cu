@@ -58,7 +58,9 @@ pwp_status pwp_linear(const pwp_linear_args* a, void* stream) {
     return PWP_EINVAL;
   if (a->rows == 0) return PWP_OK;
   if (!a->x_dev || !a->w_dev || !a->out_dev || (a->rows > 1 && a->out_stride < a->n)) return PWP_EINVAL;
-  return status_of(launch_linear_simt(*a, (cudaStream_t)stream));
+  bool used = false;
+  const cudaError_t e = launch_linear_tc(*a, (cudaStream_t)stream, &used);
+  return status_of(used || e != cudaSuccess ? e : launch_linear_simt(*a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,640 @@
+// act(x W^T + bias) (* (x W_up^T + bias_up)) + residual on the 5th-generation tensor cores
+// (bf16 operands, fp32 accumulation in tensor memory).  Both operands are stored with k
+// contiguous, the K-major form the tensor core reads, so tiles go from memory to the MMA
+// through TMA with no transpose.  Two kernels:
+//
+// pair_kernel, for many rows.  Two CTAs of a cluster share one 256 x 256 output tile
+// (tcgen05.mma.cta_group::2, M = 256, N = 256): each loads 128 rows of x and 128 rows of W per
+// 64 columns of k, half of what two CTAs with a tile each would read, and keeps the 128 x 256
+// fp32 accumulator of its own rows.  For the gated product the two CTAs' halves of W are 128
+// rows of W and the same 128 rows of W_up: a CTA's accumulator then holds both sums of an
+// output element (columns c and 128 + c of one lane) and the product needs no exchange.  Two
+// accumulators alternate, so the epilogue of a tile runs beside the next tile's MMAs.
+//
+// skinny_kernel, for few rows, where the weights' bytes bound the time: the roles are swapped
+// (128 rows of W are the M side, up to 256 rows of x the N side, padded to 16), k is split
+// over the CTAs of a cluster so that every SM streams weights, and the partial sums are
+// added through distributed shared memory in rank order -- no atomics, no workspace.
+//
+// Accumulators are fp32; bias, activation, product and residual are applied in fp32 and the
+// result is rounded to bf16 once.  Every wait is bounded: a wait that runs out records
+// PWP_ETIMEOUT and the rows concerned come out NaN; copies and MMAs in flight are waited for
+// before a CTA leaves.
+#include "block_ops.cuh"
+#include "tc_common.cuh"
+
+namespace pwp {
+namespace {
+
+using namespace tc;
+typedef __nv_bfloat16 bf16;
+
+constexpr int TK = 64;                            // k per stage: one 128-byte swizzled row
+constexpr int ROW_BYTES = TK * 2;
+
+// ---------------------------------------------------------------- cluster helpers
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the address, in the cluster's window, of a shared-memory address of this CTA as CTA `rank` has it
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void remote_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ float2 remote_load2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+// A tile load of a CTA pair: into this CTA's shared memory, counted by the barrier at `bar`
+// (a cluster address: the leader's).
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, "
+      "%4}], [%2];" ::"r"(dst),
+      "l"((uint64_t)map), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(da), "l"(db), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_one(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(da), "l"(db), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// D fp32, A and B bf16 and K-major
+__host__ __device__ constexpr uint32_t idesc_bf16(int m, int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// ---------------------------------------------------------------- epilogue pieces
+
+struct Epilogue {
+  const bf16* bias;
+  const bf16* bias_up;
+  const bf16* residual;
+  bf16* out;
+  long long residual_stride, out_stride;
+  int act;
+};
+
+__device__ __forceinline__ void unpack8(uint4 u, float* v) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// v[i] += p[i], i < avail (avail > 0); 16-byte loads when all 32 are there and p allows it
+__device__ __forceinline__ void add32(float (&v)[32], const bf16* p, int avail) {
+  if (avail >= 32 && ((uintptr_t)p & 15) == 0) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float t[8];
+      unpack8(*reinterpret_cast<const uint4*>(p + 8 * q), t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[8 * q + i] += t[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < avail) v[i] += to_f32(p[i]);
+  }
+}
+__device__ __forceinline__ void store32(bf16* p, const float (&v)[32], int avail) {
+  if (avail >= 32 && ((uintptr_t)p & 15) == 0) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<uint4*>(p + 8 * q) =
+          make_uint4(pack2(v[8 * q], v[8 * q + 1]), pack2(v[8 * q + 2], v[8 * q + 3]),
+                     pack2(v[8 * q + 4], v[8 * q + 5]), pack2(v[8 * q + 6], v[8 * q + 7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < avail) p[i] = from_f32<bf16>(v[i]);
+  }
+}
+// One switch per 32 values, not per value.
+__device__ __forceinline__ void activate32(int act, float (&v)[32]) {
+  switch (act) {
+    case PWP_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = activate(PWP_ACT_RELU, v[i]);
+      break;
+    case PWP_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = activate(PWP_ACT_SILU, v[i]);
+      break;
+    case PWP_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = activate(PWP_ACT_GELU, v[i]);
+      break;
+    case PWP_ACT_GELU_TANH:
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = activate(PWP_ACT_GELU_TANH, v[i]);
+      break;
+    default: break;
+  }
+}
+
+// ---------------------------------------------------------------- many rows
+
+constexpr int P_ROWS = 128;                       // rows of x, and of W, per CTA
+constexpr int P_STAGES = 7;
+constexpr int P_STAGE_BYTES = 2 * P_ROWS * ROW_BYTES;   // 32 KB
+constexpr int P_SMEM = P_STAGES * P_STAGE_BYTES + 1024 + 256;
+constexpr int P_EPI_WARPS = 4, P_THREADS = 32 * (2 + P_EPI_WARPS);
+constexpr int P_ACC_COLS = 256;
+constexpr int P_GROUP = 8;                        // row tiles that share W tiles while they are in L2
+
+// Tile t of the raster: groups of P_GROUP row tiles, inside a group the row tile runs fastest.
+__device__ __forceinline__ void pair_tile(int t, int mt, int nt, int& m, int& n) {
+  const int per = P_GROUP * nt;
+  const int g = t / per, r = t - g * per;
+  const int rows = min(P_GROUP, mt - g * P_GROUP);
+  n = r / rows;
+  m = g * P_GROUP + (r - n * rows);
+}
+
+template <bool GATED>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
+    pair_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
+                const __grid_constant__ CUtensorMap umap, long long rows, int n, int nk, Epilogue ep, pwp_stats* st,
+                long long spin) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + P_STAGES * P_STAGE_BYTES);   // the leader's are used
+  uint64_t* empty = full + P_STAGES;
+  uint64_t* afull = empty + P_STAGES;
+  uint64_t* aempty = afull + 2;                                                    // the leader's are used
+  uint64_t* drain = aempty + 2;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  volatile int* abortp = &abort_flag;
+
+  constexpr int NT = GATED ? 128 : 256;           // output columns of a tile
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int mt = (int)((rows + 2 * P_ROWS - 1) / (2 * P_ROWS)), nt = (n + NT - 1) / NT;
+  const int tiles = mt * nt, pairs = gridDim.x / 2, first = blockIdx.x / 2;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < P_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&afull[a], 1);
+      mbar_init(&aempty[a], 2 * P_EPI_WARPS);
+    }
+    mbar_init(drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    abort_flag = 0;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                 "r"(2 * P_ACC_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  cluster_sync();
+  fence_after();
+  pdl_enter();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      prefetch_map(&xmap);
+      prefetch_map(&wmap);
+      const uint32_t sbase = smem_u32(smem);
+      long long it = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += pairs) {
+        int m, c;
+        pair_tile(t, mt, nt, m, c);
+        const int y = m * 2 * P_ROWS + (int)rank * P_ROWS;
+        const CUtensorMap* bmap = GATED && rank ? &umap : &wmap;
+        const int yb = GATED ? c * NT : c * NT + (int)rank * P_ROWS;
+        for (int kt = 0; kt < nk; ++kt, ++it) {
+          const int s = (int)(it % P_STAGES);
+          if (it >= P_STAGES && !mbar_wait(&empty[s], (uint32_t)((it / P_STAGES) - 1) & 1, abortp, spin)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
+          if (rank == 0) mbar_expect_tx(&full[s], 2 * P_STAGE_BYTES);
+          const uint32_t dst = sbase + s * P_STAGE_BYTES;
+          tma_load_pair(dst, &xmap, bar, kt * TK, y);
+          tma_load_pair(dst + P_ROWS * ROW_BYTES, bmap, bar, kt * TK, yb);
+        }
+      }
+      if (!ok) *abortp = 1;
+      // both CTAs' copies land before either leaves: they are counted by the leader's barriers
+      if (rank == 0)
+        for (long long i = it > P_STAGES ? it - P_STAGES : 0; i < it; ++i)
+          mbar_wait(&full[i % P_STAGES], (uint32_t)(i / P_STAGES) & 1, kDrainLimit);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      const uint32_t sbase = smem_u32(smem);
+      constexpr uint32_t idesc = idesc_bf16(256, 256);
+      long long it = 0;
+      int i = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += pairs, ++i) {
+        const int a = i & 1;
+        if (i >= 2 && !mbar_wait(&aempty[a], (uint32_t)((i >> 1) - 1) & 1, abortp, spin)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        const uint32_t d = tmem + (uint32_t)(a * P_ACC_COLS);
+        for (int kt = 0; kt < nk; ++kt, ++it) {
+          const int s = (int)(it % P_STAGES);
+          if (!mbar_wait(&full[s], (uint32_t)(it / P_STAGES) & 1, abortp, spin)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          const uint32_t pa = sbase + s * P_STAGE_BYTES, pb = pa + P_ROWS * ROW_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < TK / 16; ++kk)
+            mma_pair(d, sw128_desc(pa + kk * 32, 16, 1024), sw128_desc(pb + kk * 32, 16, 1024), idesc, (kt | kk) != 0);
+          commit_pair(&empty[s]);
+        }
+        if (ok) commit_pair(&afull[a]);
+      }
+      if (!ok) *abortp = 1;
+      commit_pair(drain);      // every MMA issued has finished before tensor memory is released
+      mbar_wait(drain, 0, kDrainLimit);
+    }
+    __syncwarp();
+  } else {
+    const int quarter = warp & 3;
+    int i = 0;
+    bool ok = true;
+    for (int t = first; t < tiles; t += pairs, ++i) {
+      const int a = i & 1;
+      if (ok) {
+        ok = mbar_wait(&afull[a], (uint32_t)(i >> 1) & 1, abortp, spin);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok && lane == 0) {
+          *abortp = 1;
+          if (st) set_error(st, PWP_ETIMEOUT, kSiteLinear);
+        }
+      }
+      fence_after();
+      int m, c;
+      pair_tile(t, mt, nt, m, c);
+      const long long r = (long long)m * 2 * P_ROWS + rank * P_ROWS + quarter * 32 + lane;
+      const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(a * P_ACC_COLS);
+#pragma unroll 1
+      for (int ch = 0; ch < NT / 32; ++ch) {
+        const int c0 = c * NT + ch * 32, avail = n - c0;
+        if (avail <= 0) break;
+        float v[32], u[32];
+        tmem_ld32(base + (uint32_t)(ch * 32), v);
+        if (GATED) tmem_ld32(base + (uint32_t)(128 + ch * 32), u);
+        if (ep.bias) add32(v, ep.bias + c0, avail);
+        activate32(ep.act, v);
+        if (GATED) {
+          if (ep.bias_up) add32(u, ep.bias_up + c0, avail);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] *= u[j];
+        }
+        if (r < rows) {
+          if (ep.residual) add32(v, ep.residual + r * ep.residual_stride + c0, avail);
+          if (!ok) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __int_as_float(0x7fc00000);
+          }
+          store32(ep.out + r * ep.out_stride + c0, v, avail);
+        }
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) remote_arrive(map_rank(smem_u32(&aempty[a]), 0));
+    }
+  }
+
+  fence_before();
+  __syncthreads();
+  cluster_sync();       // the peer's copies, MMAs and arrivals on this CTA's barriers are done
+  fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * P_ACC_COLS) : "memory");
+}
+
+// ---------------------------------------------------------------- few rows
+
+constexpr int S_FEATURES = 128;                   // rows of W (and W_up) per CTA
+constexpr int S_MAX_STAGES = 8, S_THREADS = 256;
+constexpr int S_MAX_CLUSTER = 8;
+
+struct Skinny {
+  int rows, n, nk;
+  int npad;            // rows of x per tile, a multiple of 16 (the tile's tensor-memory columns)
+  int row_tiles, split, stages, tmem_cols;
+};
+
+template <bool GATED>
+__global__ void __launch_bounds__(S_THREADS, 1)
+    skinny_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
+                  const __grid_constant__ CUtensorMap umap, const Skinny g, const Epilogue ep, pwp_stats* st,
+                  long long spin) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  __shared__ uint64_t full[S_MAX_STAGES], empty[S_MAX_STAGES], done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  volatile int* abortp = &abort_flag;
+
+  constexpr int F = GATED ? S_FEATURES / 2 : S_FEATURES;   // output columns of a tile
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)(blockIdx.x % g.split), tile = (int)(blockIdx.x / g.split);
+  const int c0 = (tile / g.row_tiles) * F, r0 = (tile % g.row_tiles) * g.npad;
+  const int kt0 = (int)((long long)g.nk * rank / g.split), kt1 = (int)((long long)g.nk * (rank + 1) / g.split);
+  const int stage_bytes = (S_FEATURES + g.npad) * ROW_BYTES;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < g.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    abort_flag = 0;
+  }
+  if (warp == 1) tmem_alloc(&tmem_slot, (uint32_t)g.tmem_cols);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_slot;
+  pdl_enter();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int issued = 0;
+      for (int kt = kt0; kt < kt1; ++kt, ++issued) {
+        const int s = issued % g.stages;
+        if (issued >= g.stages && !mbar_wait(&empty[s], (uint32_t)(issued / g.stages - 1) & 1, abortp, spin)) {
+          *abortp = 1;
+          break;
+        }
+        mbar_expect_tx(&full[s], (uint32_t)stage_bytes);
+        uint8_t* a = smem + s * stage_bytes;
+        tma_load_2d(a, &wmap, &full[s], kt * TK, c0);
+        tma_load_2d(a + 64 * ROW_BYTES, GATED ? &umap : &wmap, &full[s], kt * TK, GATED ? c0 : c0 + 64);
+        tma_load_2d(a + S_FEATURES * ROW_BYTES, &xmap, &full[s], kt * TK, r0);
+      }
+      for (int i = issued > g.stages ? issued - g.stages : 0; i < issued; ++i)
+        mbar_wait(&full[i % g.stages], (uint32_t)(i / g.stages) & 1, kDrainLimit);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t sbase = smem_u32(smem), idesc = idesc_bf16(S_FEATURES, g.npad);
+      bool ok = true;
+      for (int kt = kt0, i = 0; kt < kt1; ++kt, ++i) {
+        const int s = i % g.stages;
+        if (!mbar_wait(&full[s], (uint32_t)(i / g.stages) & 1, abortp, spin)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        const uint32_t pa = sbase + s * stage_bytes, pb = pa + S_FEATURES * ROW_BYTES;
+#pragma unroll
+        for (int kk = 0; kk < TK / 16; ++kk)
+          mma_one(tmem, sw128_desc(pa + kk * 32, 16, 1024), sw128_desc(pb + kk * 32, 16, 1024), idesc, (i | kk) != 0);
+        mma_commit(&empty[s]);
+      }
+      if (!ok) *abortp = 1;
+      mma_commit(&done);
+      mbar_wait(&done, 0, kDrainLimit);
+    }
+    __syncwarp();
+  }
+  fence_before();
+  __syncthreads();      // every copy has landed, every MMA has finished: the stages are free
+  fence_after();
+
+  // This CTA's partial sums, [row of x][feature], lane = feature: consecutive addresses.
+  const bool failed_tile = *abortp != 0;
+  float* part = reinterpret_cast<float*>(smem);
+  const int quarter = warp & 3;
+  for (int j = (warp >> 2) * 16; j < g.npad; j += 32) {
+    float v[16];
+    tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)j, v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      part[(j + i) * S_FEATURES + quarter * 32 + lane] = failed_tile ? __int_as_float(0x7fc00000) : v[i];
+  }
+  if (failed_tile && threadIdx.x == 0 && st) set_error(st, PWP_ETIMEOUT, kSiteLinear);
+  fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_free(tmem, (uint32_t)g.tmem_cols);
+  if (g.split > 1) cluster_sync();
+
+  // Rank r of the cluster finishes its share of the tile's outputs, two columns a thread.
+  const int have = min(g.npad, g.rows - r0), pairs = have * (F / 2);
+  const int e0 = (int)((long long)pairs * rank / g.split), e1 = (int)((long long)pairs * (rank + 1) / g.split);
+  const uint32_t pbase = smem_u32(part);
+  for (int e = e0 + threadIdx.x; e < e1; e += S_THREADS) {
+    const int t = e / (F / 2), f = 2 * (e % (F / 2)), c = c0 + f;
+    if (c >= g.n) continue;
+    const uint32_t at = pbase + (uint32_t)(t * S_FEATURES + f) * 4u;
+    float2 v = make_float2(0.f, 0.f), u = v;
+    for (int q = 0; q < g.split; ++q) {
+      const uint32_t from = g.split > 1 ? map_rank(at, (uint32_t)q) : at;
+      const float2 p = remote_load2(from);
+      v.x += p.x;
+      v.y += p.y;
+      if (GATED) {
+        const float2 pu = remote_load2(from + 64 * 4);
+        u.x += pu.x;
+        u.y += pu.y;
+      }
+    }
+    const bool two = c + 1 < g.n;
+    if (ep.bias) {
+      v.x += to_f32(ep.bias[c]);
+      if (two) v.y += to_f32(ep.bias[c + 1]);
+    }
+    v.x = activate(ep.act, v.x);
+    v.y = activate(ep.act, v.y);
+    if (GATED) {
+      if (ep.bias_up) {
+        u.x += to_f32(ep.bias_up[c]);
+        if (two) u.y += to_f32(ep.bias_up[c + 1]);
+      }
+      v.x *= u.x;
+      v.y *= u.y;
+    }
+    const long long r = r0 + t;
+    if (ep.residual) {
+      const bf16* p = ep.residual + r * ep.residual_stride + c;
+      v.x += to_f32(p[0]);
+      if (two) v.y += to_f32(p[1]);
+    }
+    bf16* o = ep.out + r * ep.out_stride + c;
+    if (two && ((uintptr_t)o & 3) == 0) {
+      *reinterpret_cast<uint32_t*>(o) = pack2(v.x, v.y);
+    } else {
+      o[0] = from_f32<bf16>(v.x);
+      if (two) o[1] = from_f32<bf16>(v.y);
+    }
+  }
+  if (g.split > 1) cluster_sync();      // the others have read this CTA's sums
+}
+
+// ---------------------------------------------------------------- host side
+
+// [height][k] bf16, row stride in elements, tiles of box_rows x 64; false when the copies
+// cannot take it
+bool make_map(CUtensorMap* map, const void* p, long long height, int k, long long stride, int box_rows) {
+  if (height <= 1) stride = (k + 7) & ~7;       // a single row: its stride is never used
+  if (((uintptr_t)p & 15) || (stride & 7) || stride < k || stride >= (1LL << 38) || height >= (1LL << 32)) return false;
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (!encode) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)height};
+  cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+  cuuint32_t box[2] = {(cuuint32_t)TK, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool GATED>
+cudaError_t run_pair(const pwp_linear_args& a, const Epilogue& ep, cudaStream_t s, bool* used) {
+  CUtensorMap xm, wm, um;
+  if (!make_map(&xm, a.x_dev, a.rows, a.k, a.x_stride, P_ROWS) || !make_map(&wm, a.w_dev, a.n, a.k, a.w_stride, P_ROWS))
+    return cudaSuccess;
+  um = wm;
+  if (GATED && !make_map(&um, a.w_up_dev, a.n, a.k, a.w_up_stride, P_ROWS)) return cudaSuccess;
+  static std::atomic<unsigned long long> attr_done{0};
+  if (first_on_device(attr_done)) {
+    cudaError_t e = cudaFuncSetAttribute(pair_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM);
+    if (e != cudaSuccess) return e;
+  }
+  constexpr int NT = GATED ? 128 : 256;
+  const long long tiles = ((a.rows + 2 * P_ROWS - 1) / (2 * P_ROWS)) * ((a.n + NT - 1) / NT);
+  if (tiles > 0x3fffffffLL) return cudaSuccess;
+  const int pairs = tiles < kNumSM / 2 ? (int)tiles : kNumSM / 2;
+  *used = true;
+  const cudaError_t e = launch_pdl(pair_kernel<GATED>, dim3(2 * pairs), dim3(P_THREADS), (size_t)P_SMEM, s, xm, wm, um,
+                                   (long long)a.rows, a.n, (a.k + TK - 1) / TK, ep, a.stats_dev, wait_limit());
+  count_launches(1);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+template <bool GATED>
+cudaError_t run_skinny(const pwp_linear_args& a, const Epilogue& ep, cudaStream_t s, bool* used) {
+  constexpr int F = GATED ? S_FEATURES / 2 : S_FEATURES;
+  Skinny g;
+  g.rows = (int)a.rows;
+  g.n = a.n;
+  g.nk = (a.k + TK - 1) / TK;
+  g.row_tiles = (g.rows + 255) / 256;
+  g.npad = (((g.rows + g.row_tiles - 1) / g.row_tiles) + 15) & ~15;
+  g.row_tiles = (g.rows + g.npad - 1) / g.npad;
+  g.tmem_cols = 32;
+  while (g.tmem_cols < g.npad) g.tmem_cols *= 2;
+  const int stage_bytes = (S_FEATURES + g.npad) * ROW_BYTES;
+  const long long tiles = (long long)((a.n + F - 1) / F) * g.row_tiles;
+  // up to 64 rows two CTAs fit an SM
+  const int per_sm = g.npad <= 64 ? 2 : 1;
+  const int budget = (per_sm == 2 ? 112 : 224) * 1024 - 1024;
+  g.stages = budget / stage_bytes < S_MAX_STAGES ? budget / stage_bytes : S_MAX_STAGES;
+  const long long slots = (long long)kNumSM * per_sm;
+  long long split = slots / tiles;
+  if (split > S_MAX_CLUSTER) split = S_MAX_CLUSTER;
+  if (split > g.nk) split = g.nk;
+  if (split < 1) split = 1;
+  g.split = (int)split;
+  if (tiles * split > 0x7fffffffLL) return cudaSuccess;
+  int smem = g.stages * stage_bytes;
+  const int parts = g.npad * S_FEATURES * (int)sizeof(float);
+  if (smem < parts) smem = parts;
+  smem += 1024;
+  CUtensorMap xm, wm, um;
+  if (!make_map(&xm, a.x_dev, a.rows, a.k, a.x_stride, g.npad) || !make_map(&wm, a.w_dev, a.n, a.k, a.w_stride, 64))
+    return cudaSuccess;
+  um = wm;
+  if (GATED && !make_map(&um, a.w_up_dev, a.n, a.k, a.w_up_stride, 64)) return cudaSuccess;
+  static std::atomic<unsigned long long> attr_done{0};
+  if (first_on_device(attr_done)) {
+    cudaError_t e = cudaFuncSetAttribute(skinny_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * split));
+  cfg.blockDim = dim3(S_THREADS);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  *used = true;
+  const cudaError_t e =
+      cudaLaunchKernelEx(&cfg, skinny_kernel<GATED>, xm, wm, um, g, ep, a.stats_dev, wait_limit());
+  count_launches(1);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+}  // namespace
+
+// Declines (used = false) when the tensors do not meet the copies' rules (16-byte aligned
+// bases, row strides a multiple of 16 bytes).
+cudaError_t launch_linear_tc(const pwp_linear_args& a, cudaStream_t s, bool* used) {
+  *used = false;
+  if (a.type != PWP_BF16) return cudaSuccess;
+  const Epilogue ep{(const bf16*)a.bias_dev, (const bf16*)a.bias_up_dev, (const bf16*)a.residual_dev, (bf16*)a.out_dev,
+                    a.residual_stride, a.out_stride, a.activation};
+  const bool gated = a.w_up_dev != nullptr;
+  // Too few 256-row tiles to fill the SMs' pairs: split k instead.
+  const long long tiles = ((a.rows + 255) / 256) * ((a.n + (gated ? 127 : 255)) / (gated ? 128 : 256));
+  const bool skinny = a.rows <= 128 || tiles <= 48;
+  if (skinny) return gated ? run_skinny<true>(a, ep, s, used) : run_skinny<false>(a, ep, s, used);
+  return gated ? run_pair<true>(a, ep, s, used) : run_pair<false>(a, ep, s, used);
+}
+
+}  // namespace pwp
