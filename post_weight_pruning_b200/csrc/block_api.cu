@@ -47,7 +47,9 @@ pwp_status pwp_attention(const pwp_attention_args* a, void* stream) {
     if (a->q_stride[i] < 0 || a->k_stride[i] < 0 || a->v_stride[i] < 0 || a->out_stride[i] < 0) return PWP_EINVAL;
   if (a->n == 0 || a->nseq == 0) return PWP_OK;
   if (!a->q_dev || !a->k_dev || !a->v_dev || !a->out_dev || !a->cu_seqlens_dev) return PWP_EINVAL;
-  return status_of(launch_attention_simt(*a, (cudaStream_t)stream));
+  bool used = false;
+  const cudaError_t e = launch_attention_tc(*a, (cudaStream_t)stream, &used);
+  return status_of(used || e != cudaSuccess ? e : launch_attention_simt(*a, (cudaStream_t)stream));
 }
 
 pwp_status pwp_linear(const pwp_linear_args* a, void* stream) {

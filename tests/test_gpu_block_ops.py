@@ -417,6 +417,29 @@ def test_operators_on_a_stream_of_their_own_and_in_a_graph():
         assert all(torch.equal(a, b) for a, b in zip(kept, want))
 
 
+def test_waits_that_run_out_are_reported():
+    torch, pwp = _torch(), _pwp()
+    q, k, v, cu = att_case([200], 2, 1, 128, "bf16", 101)
+    w = rnd((512, 512), "bf16", 103)
+    xs = [rnd((r, 512), "bf16", 102) for r in (4, 2048)]
+    want = [pwp.attention(q, k, v, cu)] + [pwp.linear(x, w) for x in xs]
+    torch.cuda.synchronize()
+    calls = [(lambda st: pwp.attention(q, k, v, cu, stats=st), 9)] + \
+            [(lambda st, x=x: pwp.linear(x, w, stats=st), 10) for x in xs]
+    for (call, site), ok in zip(calls, want):
+        prev = pwp.set_wait_limit(0)
+        try:
+            st = pwp.new_stats()
+            call(st)
+            torch.cuda.synchronize()
+        finally:
+            pwp.set_wait_limit(prev)
+        s = pwp.read_stats(st)
+        assert (s.status, s.status_site) == (5, site)
+        st = pwp.new_stats()
+        assert torch.equal(call(st), ok) and pwp.read_stats(st).status == 0
+
+
 # ------------------------------------------------------------------- the block
 
 def _block(dtype, heads, kv, width, ff, n, seed=111):
