@@ -17,6 +17,7 @@ import ctypes
 import functools
 import inspect
 import math
+import struct
 
 import numpy as np
 
@@ -31,32 +32,17 @@ FEEDS = {"q_proj": "attn_in", "k_proj": "attn_in", "v_proj": "attn_in", "o_proj"
          "up_proj": "mlp_in", "down_proj": "down_in"}
 
 
-class RopeArgs(ctypes.Structure):
-    _fields_ = [("q", _vp), ("k", _vp), ("q_out", _vp), ("k_out", _vp), ("q_stride", _i64 * 2), ("k_stride", _i64 * 2),
-                ("q_out_stride", _i64 * 2), ("k_out_stride", _i64 * 2), ("positions", _vp), ("freqs", _vp),
-                ("q_weight", _vp), ("k_weight", _vp), ("n", _i64), ("type", _i32), ("hq", _i32), ("hk", _i32),
-                ("d", _i32), ("rot", _i32), ("layout", _i32), ("eps", _f32), ("factor", _f32)]
-
-
-class AttentionArgs(ctypes.Structure):
-    _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("out", _vp), ("q_stride", _i64 * 2), ("k_stride", _i64 * 2),
-                ("v_stride", _i64 * 2), ("out_stride", _i64 * 2), ("cu_seqlens", _vp), ("stats", _vp), ("n", _i64),
-                ("nseq", _i32), ("type", _i32), ("hq", _i32), ("hk", _i32), ("d", _i32), ("causal", _i32),
-                ("scale", _f32)]
-
-
-class LinearArgs(ctypes.Structure):
-    _fields_ = [("x", _vp), ("w", _vp), ("w_up", _vp), ("bias", _vp), ("bias_up", _vp), ("residual", _vp),
-                ("out", _vp), ("x_stride", _i64), ("w_stride", _i64), ("w_up_stride", _i64),
-                ("residual_stride", _i64), ("out_stride", _i64), ("stats", _vp), ("rows", _i64), ("k", _i32),
-                ("n", _i32), ("type", _i32), ("activation", _i32)]
-
+# pwp_rope_args, pwp_attention_args and pwp_linear_args field by field, packed in one call: a
+# small operator's time is mostly its host side
+ROPE_ARGS = struct.Struct("@4P8q4Pq6i2f")
+ATTENTION_ARGS = struct.Struct("@4P8q2Pq6if4x")
+LINEAR_ARGS = struct.Struct("@7P5qPq4i")
 
 SIGNATURES = {
     "pwp_rms_norm": (_i32, [_vp, _i32, _i64, _i32, _i64, _vp, _f32, _vp, _i64, _vp]),
-    "pwp_qk_norm_rope": (_i32, [ctypes.POINTER(RopeArgs), _vp]),
-    "pwp_attention": (_i32, [ctypes.POINTER(AttentionArgs), _vp]),
-    "pwp_linear": (_i32, [ctypes.POINTER(LinearArgs), _vp]),
+    "pwp_qk_norm_rope": (_i32, [ctypes.c_char_p, _vp]),
+    "pwp_attention": (_i32, [ctypes.c_char_p, _vp]),
+    "pwp_linear": (_i32, [ctypes.c_char_p, _vp]),
 }
 
 
@@ -70,38 +56,57 @@ def _operator(fn):
 
     @functools.wraps(fn)
     def wrapped(*a, **kw):
-        torch = _pwp._torch()
         x = a[0] if a else kw.get(first)
-        if not torch.is_tensor(x):
-            raise TypeError(f"{fn.__name__}: {first}: tensor expected, got {type(x).__name__}")
+        try:
+            dev = x.get_device()
+        except AttributeError:
+            raise TypeError(f"{fn.__name__}: {first}: tensor expected, got {type(x).__name__}") from None
         call = fn if kw.get("stream") is None else on_stream
-        if not x.is_cuda or x.device.index == torch.cuda.current_device():
+        torch = _pwp._torch()
+        if dev < 0 or dev == torch.cuda.current_device():
             return call(*a, **kw)
-        with torch.cuda.device(x.device):
+        with torch.cuda.device(dev):
             return call(*a, **kw)
     return wrapped
+
+
+def _on_gpu(t):
+    return t.is_cuda
+
+
+def _stream_of(dev):
+    return _pwp._torch()._C._cuda_getCurrentRawStream(dev)
+
+
+def _type_code(x, name, dims):
+    """PWP_BF16 or PWP_FP32 of an operator's first tensor, whose form is checked."""
+    torch = _pwp._torch()
+    code = _pwp.BF16 if x.dtype is torch.bfloat16 else _pwp.FP32 if x.dtype is torch.float32 else None
+    if code is None:
+        _pwp._dtype_code(x)       # raises
+    if x.dim() != dims:
+        raise ValueError(f"{name}: {dims} dimensions expected, got shape {tuple(x.shape)}")
+    if not _on_gpu(x):
+        raise ValueError(f"{name}: CUDA tensors expected")
+    if x.stride(-1) != 1 and x.shape[-1] > 1:
+        raise ValueError(f"{name}: elements of the last dimension must be contiguous")
+    return code
 
 
 def _check_tensor(t, name, shape, like, dtype=None):
     """`t` on the device of `like`, of its element type (or `dtype`) and of `shape`, with
     contiguous elements in its last dimension."""
+    if dtype is None:
+        dtype = like.dtype
+    if t.dtype is dtype and t.shape == shape and t.get_device() == like.get_device() and t.stride(-1) == 1:
+        return
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != (dtype or like.dtype):
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype or like.dtype}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.device != like.device:
         raise ValueError(f"{name}: on {t.device}, the first tensor on {like.device}")
-    if t.shape and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: elements of the last dimension must be contiguous")
-
-
-def _check_first(t, name, dims):
-    _pwp._dtype_code(t)
-    if t.dim() != dims:
-        raise ValueError(f"{name}: {dims} dimensions expected, got shape {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: CUDA tensors expected")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.shape[-1] > 1:
         raise ValueError(f"{name}: elements of the last dimension must be contiguous")
 
 
@@ -116,8 +121,7 @@ def _check_out(t, name, shape, like):
 
 
 def _forward_only(*ts):
-    torch = _pwp._torch()
-    if torch.is_grad_enabled():
+    if _pwp._torch().is_grad_enabled():
         for t in ts:
             if t is not None and t.requires_grad:
                 raise ValueError("the operators compute a forward pass only: call them under torch.no_grad() "
@@ -125,18 +129,18 @@ def _forward_only(*ts):
 
 
 def _ptr(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
 def _stats_ptr(stats, like):
-    if stats is not None:
-        torch = _pwp._torch()
-        _check_tensor(stats, "stats", (ctypes.sizeof(_pwp.Stats),), like, torch.uint8)
-    return _ptr(stats)
+    if stats is None:
+        return 0
+    _check_tensor(stats, "stats", (ctypes.sizeof(_pwp.Stats),), like, _pwp._torch().uint8)
+    return stats.data_ptr()
 
 
-def _call(name, args):
-    st = getattr(_pwp.lib(), name)(ctypes.byref(args), _pwp._stream_ptr())
+def _call(name, args, dev):
+    st = getattr(_pwp.lib(), name)(args, _stream_of(dev))
     if st:
         raise _pwp.PwpError(st, name)
 
@@ -147,9 +151,8 @@ def _call(name, args):
 def rms_norm(x, weight=None, *, eps=1e-5, out=None, stream=None):
     """x / sqrt(mean(x^2) + eps) * weight over the rows of x ([n, width], bf16 or fp32;
     rows may be strided).  weight: [width] or None.  out: None, a tensor like x, or x itself."""
-    torch = _pwp._torch()
-    _check_first(x, "x", 2)
-    n, width = x.shape
+    code = _type_code(x, "x", 2)
+    n, width = shape = x.shape
     if width < 1 or width > 65536:
         raise ValueError(f"x: width {width}, 1 to 65536 expected")
     if weight is not None:
@@ -158,13 +161,14 @@ def rms_norm(x, weight=None, *, eps=1e-5, out=None, stream=None):
         raise ValueError(f"eps: {eps}")
     _forward_only(x, weight)
     if out is None:
-        out = torch.empty((n, width), dtype=x.dtype, device=x.device)
+        out = x.new_empty(shape)
     elif out is not x:
-        _check_out(out, "out", (n, width), x)
+        _check_out(out, "out", shape, x)
     if n:
-        st = _pwp.lib().pwp_rms_norm(x.data_ptr(), _pwp._dtype_code(x), n, width, x.stride(0), _ptr(weight),
-                                     float(eps), out.data_ptr(), out.stride(0), _pwp._stream_ptr())
-        _pwp._check(st, "pwp_rms_norm")
+        st = _pwp.lib().pwp_rms_norm(x.data_ptr(), code, n, width, x.stride(0), _ptr(weight), eps, out.data_ptr(),
+                                     out.stride(0), _stream_of(x.get_device()))
+        if st:
+            raise _pwp.PwpError(st, "pwp_rms_norm")
     return out
 
 
@@ -236,12 +240,13 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     elements i and i + rot/2, "interleaved" 2i and 2i+1.  q_out / k_out: None, tensors of the
     same shapes, or q / k themselves.  Returns (q_out, k_out)."""
     torch = _pwp._torch()
-    _check_first(q, "q", 3)
-    n, hq, d = q.shape
+    code = _type_code(q, "q", 3)
+    n, hq, d = q_shape = q.shape
     if k.dim() != 3:
         raise ValueError(f"k: [n, heads, d] expected, got shape {tuple(k.shape)}")
     hk = k.shape[1]
-    _check_tensor(k, "k", (n, hk, d), q)
+    k_shape = (n, hk, d)
+    _check_tensor(k, "k", k_shape, q)
     _check_tensor(positions, "positions", (n,), q, torch.int64)
     if freqs.dim() != 1:
         raise ValueError(f"freqs: one dimension expected, got shape {tuple(freqs.shape)}")
@@ -253,27 +258,25 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
         raise ValueError(f"layout: {layout!r}, one of {sorted(LAYOUTS)} expected")
     if not (eps >= 0 and math.isfinite(eps) and math.isfinite(factor)):
         raise ValueError(f"eps {eps}, factor {factor}")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _check_tensor(w, name, (d,), q)
+    if q_weight is not None:
+        _check_tensor(q_weight, "q_weight", (d,), q)
+    if k_weight is not None:
+        _check_tensor(k_weight, "k_weight", (d,), q)
     _forward_only(q, k, q_weight, k_weight)
     if q_out is None:
-        q_out = torch.empty((n, hq, d), dtype=q.dtype, device=q.device)
+        q_out = q.new_empty(q_shape)
     elif q_out is not q:
-        _check_out(q_out, "q_out", (n, hq, d), q)
+        _check_out(q_out, "q_out", q_shape, q)
     if k_out is None:
-        k_out = torch.empty((n, hk, d), dtype=q.dtype, device=q.device)
+        k_out = q.new_empty(k_shape)
     elif k_out is not k:
-        _check_out(k_out, "k_out", (n, hk, d), q)
+        _check_out(k_out, "k_out", k_shape, q)
     if n and hq + hk:
-        if positions.stride(0) != 1 and n > 1:
-            raise ValueError("positions: contiguous tensor expected")
-        two = _i64 * 2
-        _call("pwp_qk_norm_rope", RopeArgs(
-            q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), two(q.stride(0), q.stride(1)),
-            two(k.stride(0), k.stride(1)), two(q_out.stride(0), q_out.stride(1)),
-            two(k_out.stride(0), k_out.stride(1)), positions.data_ptr(), freqs.data_ptr(), _ptr(q_weight),
-            _ptr(k_weight), n, _pwp._dtype_code(q), hq, hk, d, rot, LAYOUTS[layout], eps, factor))
+        qs, ks, qos, kos = q.stride(), k.stride(), q_out.stride(), k_out.stride()
+        _call("pwp_qk_norm_rope", ROPE_ARGS.pack(
+            q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), qs[0], qs[1], ks[0], ks[1], qos[0], qos[1],
+            kos[0], kos[1], positions.data_ptr(), freqs.data_ptr(), _ptr(q_weight), _ptr(k_weight), n, code, hq, hk, d,
+            rot, LAYOUTS[layout], eps, factor), q.get_device())
     return q_out, k_out
 
 
@@ -287,9 +290,8 @@ def attention(q, k, v, cu_seqlens, *, causal=True, scale=None, out=None, stats=N
     rows in no sequence are left as they were (of a fresh output: undefined).  Offsets that
     decrease or leave 0..n end the batch there and set status 1 in `stats` (a ``new_stats``
     record, optional), which also receives a device-side wait that ran out."""
-    torch = _pwp._torch()
-    _check_first(q, "q", 3)
-    n, hq, d = q.shape
+    code = _type_code(q, "q", 3)
+    n, hq, d = q_shape = q.shape
     if k.dim() != 3:
         raise ValueError(f"k: [n, heads, d] expected, got shape {tuple(k.shape)}")
     hk = k.shape[1]
@@ -303,30 +305,28 @@ def attention(q, k, v, cu_seqlens, *, causal=True, scale=None, out=None, stats=N
         raise ValueError(f"{n} tokens of {hq} heads: fewer than 2^31 query rows expected")
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError(f"cu_seqlens: [sequences + 1] expected, got shape {tuple(cu_seqlens.shape)}")
-    _check_tensor(cu_seqlens, "cu_seqlens", cu_seqlens.shape, q, torch.int32)
+    _check_tensor(cu_seqlens, "cu_seqlens", cu_seqlens.shape, q, _pwp._torch().int32)
     if scale is None:
         scale = d ** -0.5
-    if not math.isfinite(scale):
+    elif not math.isfinite(scale):
         raise ValueError(f"scale: {scale}")
     _forward_only(q, k, v)
     stats_p = _stats_ptr(stats, q)
     if out is None:
-        out = torch.empty((n, hq, d), dtype=q.dtype, device=q.device)
+        out = q.new_empty(q_shape)
     else:
-        _check_out(out, "out", (n, hq, d), q)
+        _check_out(out, "out", q_shape, q)
     nseq = cu_seqlens.shape[0] - 1
     if n and nseq:
-        two = _i64 * 2
-        _call("pwp_attention", AttentionArgs(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), two(q.stride(0), q.stride(1)),
-            two(k.stride(0), k.stride(1)), two(v.stride(0), v.stride(1)), two(out.stride(0), out.stride(1)),
-            cu_seqlens.data_ptr(), stats_p, n, nseq, _pwp._dtype_code(q), hq, hk, d, 1 if causal else 0, scale))
+        qs, ks, vs, os = q.stride(), k.stride(), v.stride(), out.stride()
+        _call("pwp_attention", ATTENTION_ARGS.pack(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0],
+            os[1], cu_seqlens.data_ptr(), stats_p, n, nseq, code, hq, hk, d, 1 if causal else 0, scale), q.get_device())
     return out
 
 
 def _linear(x, w, w_up, bias, bias_up, activation, residual, out, stats, name):
-    torch = _pwp._torch()
-    _check_first(x, "x", 2)
+    code = _type_code(x, "x", 2)
     rows, k = x.shape
     if w.dim() != 2:
         raise ValueError(f"{name}: [n, k] expected, got shape {tuple(w.shape)}")
@@ -336,25 +336,27 @@ def _linear(x, w, w_up, bias, bias_up, activation, residual, out, stats, name):
         raise ValueError(f"sizes out of range: {rows} rows, k {k}, n {n}")
     if w_up is not None:
         _check_tensor(w_up, "w_up", (n, k), x)
-    for nm, b in (("bias", bias), ("bias_up", bias_up)):
-        if b is not None:
-            _check_tensor(b, nm, (n,), x)
-    if activation not in ACTIVATIONS:
+    if bias is not None:
+        _check_tensor(bias, "bias", (n,), x)
+    if bias_up is not None:
+        _check_tensor(bias_up, "bias_up", (n,), x)
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation: {activation!r}, one of {sorted(ACTIVATIONS)} expected")
     if residual is not None:
         _check_tensor(residual, "residual", (rows, n), x)
     _forward_only(x, w, w_up, bias, bias_up, residual)
     stats_p = _stats_ptr(stats, x)
     if out is None:
-        out = torch.empty((rows, n), dtype=x.dtype, device=x.device)
+        out = x.new_empty((rows, n))
     else:
         _check_out(out, "out", (rows, n), x)
     if rows:
-        _call("pwp_linear", LinearArgs(
+        _call("pwp_linear", LINEAR_ARGS.pack(
             x.data_ptr(), w.data_ptr(), _ptr(w_up), _ptr(bias), _ptr(bias_up), _ptr(residual), out.data_ptr(),
             x.stride(0), w.stride(0), w_up.stride(0) if w_up is not None else 0,
-            residual.stride(0) if residual is not None else 0, out.stride(0), stats_p, rows, k, n,
-            _pwp._dtype_code(x), ACTIVATIONS[activation]))
+            residual.stride(0) if residual is not None else 0, out.stride(0), stats_p, rows, k, n, code, act),
+            x.get_device())
     return out
 
 

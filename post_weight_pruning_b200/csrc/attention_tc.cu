@@ -138,19 +138,68 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t acc) {
+// The MMAs of one tile product are issued by one elected lane of a converged warp, in one
+// statement with the operands advanced inside it: the descriptors then stay in the uniform
+// registers the instruction takes them from.  (One asm statement per MMA under a lane test
+// took 75 cycles of issue each, more than the MMA itself.)
+//
+// S (128 x 128) = Q (128 x 64 BOXES) K^T: steps of 16 are 32 bytes inside a swizzled row, a box of
+// 64 further on after four.
+template <int BOXES>
+__device__ __forceinline__ void mma_qk(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(da), "l"(db), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred q, f, t;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+      "add.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t}" ::"r"(d),
+      "l"(da), "l"(db), "r"(idesc)
       : "memory");
+  if (BOXES == 2)
+    asm volatile(
+        "{\n\t.reg .pred q, t;\n\t.reg .b64 x, y;\n\t"
+        "setp.eq.b32 t, 0, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "add.s64 x, %1, 1024;\n\tadd.s64 y, %2, 1024;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+        "add.s64 x, %1, 1026;\n\tadd.s64 y, %2, 1026;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+        "add.s64 x, %1, 1028;\n\tadd.s64 y, %2, 1028;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+        "add.s64 x, %1, 1030;\n\tadd.s64 y, %2, 1030;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t}" ::"r"(d),
+        "l"(da), "l"(db), "r"(idesc)
+        : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t ta, uint64_t db, uint32_t idesc, uint32_t acc) {
+// O += P V over 64 keys: P in tensor memory (16 keys are 8 columns), V MN-major (16 keys are
+// 2048 bytes).
+__device__ __forceinline__ void mma_pv64(uint32_t d, uint32_t ta, uint64_t db, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred q, p, t;\n\t.reg .b64 y;\n\t.reg .b32 a;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.s32 a, %1, 8;\n\tadd.s64 y, %2, 128;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %3, t;\n\t"
+      "add.s32 a, %1, 16;\n\tadd.s64 y, %2, 256;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %3, t;\n\t"
+      "add.s32 a, %1, 24;\n\tadd.s64 y, %2, 384;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %3, t;\n\t}" ::"r"(d),
       "r"(ta), "l"(db), "r"(idesc), "r"(acc)
       : "memory");
+}
+// One arrival on `bar` when the MMAs issued so far have completed (the whole warp calls it).
+__device__ __forceinline__ void commit_elected(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+// A wait the whole warp takes part in; every lane gets the same answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort, long long limit) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit));
 }
 // 32 consecutive columns of this warp's lanes, not waited for
 __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, float* v) {
@@ -307,86 +356,60 @@ __global__ void __launch_bounds__(kThreadsAtt, 1)
     const uint32_t sq = smem_u32(smem), sr = smem_u32(ring);
     constexpr uint32_t id_qk = idesc_of(KEYS, 0), id_pv = idesc_of(D, 1);
     uint32_t r = 0, fixpar = 0;
-    uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};   // q tiles, blocks, outputs so far
+    uint32_t nq = 0, np[2] = {0, 0}, no[2] = {0, 0};   // items, blocks and outputs so far
     bool ok = true;
     while (ok && next_item(a, it, x, bad)) {
-      if (lane == 0) {
-        const int nb = max(x.nb[0], x.nb[1]);
-        // S_w(0), then for every block O_w += P_w V_j and S_w(j + 1), the tiles in turn
-        for (int j = -1; j < nb && ok; ++j) {
-          const uint32_t rk = r + 2 * (uint32_t)(j + 1), rv = r + 2 * (uint32_t)j + 1;
-          const int sk = (int)(rk % C::SLOTS), sv = (int)(rv % C::SLOTS);
-          const bool any_next = j + 1 < nb;
-          bool got_k = false, got_v = false;
-          for (int w = 0; w < 2 && ok; ++w) {
-            if (j >= 0 && j < x.nb[w]) {
-              if (!got_v) {
-                ok = mbar_wait(&sb.full[sv], (rv / C::SLOTS) & 1, abortp, spin);
-                if (ok && j >= x.fix) {
-                  ok = mbar_wait(&sb.fixed[sv], (fixpar >> sv) & 1, abortp, spin);
-                  fixpar ^= 1u << sv;
-                }
-                if (!ok) break;
-                got_v = true;
-              }
-              if (j == 0 && no[w] && !mbar_wait(&sb.oempty[w], (no[w] - 1) & 1, abortp, spin)) {
-                ok = false;
-                break;
-              }
-              if (!mbar_wait(&sb.pfull[w], np[w] & 1, abortp, spin)) {
-                ok = false;
-                break;
-              }
-              ++np[w];
-              fence_after();
-              const uint32_t vb = sr + sv * C::TILE;
+      const int nb = max(x.nb[0], x.nb[1]);
+      // S_w(0), then for every block O_w += P_w V_j and S_w(j + 1), the tiles in turn
+      for (int j = -1; j < nb && ok; ++j) {
+        const uint32_t rk = r + 2 * (uint32_t)(j + 1), rv = rk - 1;
+        const int sk = (int)(rk % C::SLOTS), sv = (int)(rv % C::SLOTS);
+        const uint32_t kb = sr + sk * C::TILE, vb = sr + sv * C::TILE;
+        if (j >= 0) {
+          ok = warp_wait(&sb.full[sv], (rv / C::SLOTS) & 1, abortp, spin);
+          if (ok && j >= x.fix) {
+            ok = warp_wait(&sb.fixed[sv], (fixpar >> sv) & 1, abortp, spin);
+            fixpar ^= 1u << sv;
+          }
+        }
+        if (ok && j + 1 < nb) ok = warp_wait(&sb.full[sk], (rk / C::SLOTS) & 1, abortp, spin);
 #pragma unroll
-              for (int kk = 0; kk < KEYS / 16; ++kk)
-                mma_ts(tO + 128 * w, tS + 128 * w + 8 * kk, sw128_desc(vb + kk * 2048, BOX, 1024), id_pv, (j | kk) != 0);
+        for (int w = 0; w < 2; ++w) {
+          if (ok && j >= 0 && j < x.nb[w]) {
+            if (j == 0 && no[w]) ok = warp_wait(&sb.oempty[w], (no[w] - 1) & 1, abortp, spin);
+            ok = ok && warp_wait(&sb.pfull[w], np[w] & 1, abortp, spin);
+            ++np[w];
+            if (ok) {
+              fence_after();
+              mma_pv64(tO + 128 * w, tS + 128 * w, sw128_desc(vb, BOX, 1024), id_pv, j != 0);
+              mma_pv64(tO + 128 * w, tS + 128 * w + 32, sw128_desc(vb + 8192, BOX, 1024), id_pv, 1);
               if (j == x.nb[w] - 1) {
-                mma_commit(&sb.ofull[w]);
+                commit_elected(&sb.ofull[w]);
                 ++no[w];
               }
             }
-            if (j + 1 < x.nb[w]) {
-              if (!got_k) {
-                if (!mbar_wait(&sb.full[sk], (rk / C::SLOTS) & 1, abortp, spin)) {
-                  ok = false;
-                  break;
-                }
-                got_k = true;
-              }
-              if (j < 0) {
-                if (!mbar_wait(&sb.qfull[w], nq[w] & 1, abortp, spin)) {
-                  ok = false;
-                  break;
-                }
-                ++nq[w];
-              }
+          }
+          if (ok && j + 1 < x.nb[w]) {
+            if (j < 0) ok = warp_wait(&sb.qfull[w], (nq >> (16 * w)) & 1, abortp, spin);
+            if (ok) {
               fence_after();
-              const uint32_t qb = sq + w * C::TILE, kb = sr + sk * C::TILE;
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (uint32_t)(kk / 4) * BOX + (uint32_t)(kk % 4) * 32;
-                mma_ss(tS + 128 * w, sw128_desc(qb + off, 16, 1024), sw128_desc(kb + off, 16, 1024), id_qk, kk != 0);
-              }
-              mma_commit(&sb.sfull[w]);
-              if (j + 1 == x.nb[w] - 1) mma_commit(&sb.qempty[w]);
+              mma_qk<C::BOXES>(tS + 128 * w, sw128_desc(sq + w * C::TILE, 16, 1024), sw128_desc(kb, 16, 1024), id_qk);
+              commit_elected(&sb.sfull[w]);
+              if (j + 2 == x.nb[w]) commit_elected(&sb.qempty[w]);
             }
           }
-          if (!ok) break;
-          if (j >= 0) mma_commit(&sb.empty[sv]);
-          if (any_next) mma_commit(&sb.empty[sk]);
         }
-        r += 2 * (uint32_t)nb;
-        if (!ok) *abortp = 1;
+        if (ok && j >= 0) commit_elected(&sb.empty[sv]);
+        if (ok && j + 1 < nb) commit_elected(&sb.empty[sk]);
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      // q tiles loaded so far, one bit (the phase) per tile
+      if (x.nb[0]) nq ^= 1u;
+      if (x.nb[1]) nq ^= 1u << 16;
+      r += 2 * (uint32_t)nb;
+      if (!ok && lane == 0) *abortp = 1;
     }
-    if (lane == 0) {
-      mma_commit(&sb.drain);     // every MMA issued has finished before tensor memory is released
-      mbar_wait(&sb.drain, 0, kDrainLimit);
-    }
+    commit_elected(&sb.drain);     // every MMA issued has finished before tensor memory is released
+    mbar_wait(&sb.drain, 0, kDrainLimit);
     __syncwarp();
   } else if (warp < 4) {
     // ---------------------------------------------------------------- unseen values of V

@@ -94,6 +94,34 @@ def test_frequency_refusals(kw):
 
 # ------------------------------------------------------------------- refusals and marshalling
 
+# the argument structures of include/pwp.h, for reading packed calls and driving the C entries
+_vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("q_out", _vp), ("k_out", _vp), ("q_stride", _i64 * 2), ("k_stride", _i64 * 2),
+                ("q_out_stride", _i64 * 2), ("k_out_stride", _i64 * 2), ("positions", _vp), ("freqs", _vp),
+                ("q_weight", _vp), ("k_weight", _vp), ("n", _i64), ("type", _i32), ("hq", _i32), ("hk", _i32),
+                ("d", _i32), ("rot", _i32), ("layout", _i32), ("eps", _f32), ("factor", _f32)]
+
+
+class AttentionArgs(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("out", _vp), ("q_stride", _i64 * 2), ("k_stride", _i64 * 2),
+                ("v_stride", _i64 * 2), ("out_stride", _i64 * 2), ("cu_seqlens", _vp), ("stats", _vp), ("n", _i64),
+                ("nseq", _i32), ("type", _i32), ("hq", _i32), ("hk", _i32), ("d", _i32), ("causal", _i32),
+                ("scale", _f32)]
+
+
+class LinearArgs(ctypes.Structure):
+    _fields_ = [("x", _vp), ("w", _vp), ("w_up", _vp), ("bias", _vp), ("bias_up", _vp), ("residual", _vp),
+                ("out", _vp), ("x_stride", _i64), ("w_stride", _i64), ("w_up_stride", _i64),
+                ("residual_stride", _i64), ("out_stride", _i64), ("stats", _vp), ("rows", _i64), ("k", _i32),
+                ("n", _i32), ("type", _i32), ("activation", _i32)]
+
+
+ARGS = {"pwp_qk_norm_rope": RopeArgs, "pwp_attention": AttentionArgs, "pwp_linear": LinearArgs}
+
+
 class _FakeLib:
     def __init__(self):
         self.calls = []
@@ -103,7 +131,7 @@ class _FakeLib:
             raise AttributeError(name)
 
         def f(*a):
-            self.calls.append((name, [getattr(x, "_obj", x) for x in a]))
+            self.calls.append((name, [ARGS[name].from_buffer_copy(x) if isinstance(x, bytes) else x for x in a]))
             return 0
         return f
 
@@ -113,15 +141,8 @@ def fake(monkeypatch):
     """The library replaced by a recorder, CPU tensors let through as if they were on a GPU."""
     f = _FakeLib()
     monkeypatch.setattr(pwp, "lib", lambda: f)
-    monkeypatch.setattr(pwp, "_stream_ptr", lambda stream=None: ctypes.c_void_p(7))
-
-    def first(t, name, dims):
-        pwp._dtype_code(t)
-        if t.dim() != dims:
-            raise ValueError(name)
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError(name)
-    monkeypatch.setattr(B, "_check_first", first)
+    monkeypatch.setattr(B, "_stream_of", lambda dev: 7)
+    monkeypatch.setattr(B, "_on_gpu", lambda t: True)
     return f
 
 
@@ -271,7 +292,8 @@ def test_struct_sizes_match_the_header(tmp_path):
     subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", os.path.join(root, "include"), str(src), "-o", str(exe)],
                    check=True)
     got = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()
-    assert [int(x) for x in got] == [ctypes.sizeof(t) for t in (B.RopeArgs, B.AttentionArgs, B.LinearArgs)]
+    assert [int(x) for x in got] == [s.size for s in (B.ROPE_ARGS, B.ATTENTION_ARGS, B.LINEAR_ARGS)]
+    assert [int(x) for x in got] == [ctypes.sizeof(t) for t in ARGS.values()]
 
 
 def test_c_entry_points_check_their_arguments():
@@ -284,32 +306,32 @@ def test_c_entry_points_check_their_arguments():
     assert rms(rows=2, os=3) == 1 and rms(rows=0) == 0
 
     def att(**kw):
-        a = B.AttentionArgs(q=256, k=256, v=256, out=256, cu_seqlens=256, n=4, nseq=1, type=0, hq=2, hk=1, d=8,
+        a = AttentionArgs(q=256, k=256, v=256, out=256, cu_seqlens=256, n=4, nseq=1, type=0, hq=2, hk=1, d=8,
                             causal=1, scale=1.0)
         for key, val in kw.items():
             setattr(a, key, val)
-        return L.pwp_attention(ctypes.byref(a), None)
+        return L.pwp_attention(bytes(a), None)
     for kw in (dict(hq=3, hk=2), dict(hk=0), dict(d=257), dict(d=0), dict(n=-1), dict(n=1 << 31), dict(nseq=-1),
                dict(scale=math.inf), dict(q=None), dict(cu_seqlens=None), dict(type=3)):
         assert att(**kw) == 1, kw
     assert att(n=0) == att(nseq=0) == 0 and L.pwp_attention(None, None) == 1
 
     def lin(**kw):
-        a = B.LinearArgs(x=256, w=256, out=256, rows=2, k=4, n=4, x_stride=4, w_stride=4, out_stride=4)
+        a = LinearArgs(x=256, w=256, out=256, rows=2, k=4, n=4, x_stride=4, w_stride=4, out_stride=4)
         for key, val in kw.items():
             setattr(a, key, val)
-        return L.pwp_linear(ctypes.byref(a), None)
+        return L.pwp_linear(bytes(a), None)
     for kw in (dict(rows=-1), dict(k=0), dict(n=0), dict(k=1 << 24), dict(activation=5), dict(activation=-1), dict(x=None),
                dict(bias_up=256), dict(out_stride=3), dict(type=9)):
         assert lin(**kw) == 1, kw
     assert lin(rows=0) == 0 and L.pwp_linear(None, None) == 1
 
     def rope(**kw):
-        a = B.RopeArgs(q=256, k=256, q_out=256, k_out=256, positions=256, freqs=256, n=1, hq=1, hk=1, d=8, rot=8,
+        a = RopeArgs(q=256, k=256, q_out=256, k_out=256, positions=256, freqs=256, n=1, hq=1, hk=1, d=8, rot=8,
                        eps=1e-5, factor=1.0)
         for key, val in kw.items():
             setattr(a, key, val)
-        return L.pwp_qk_norm_rope(ctypes.byref(a), None)
+        return L.pwp_qk_norm_rope(bytes(a), None)
     for kw in (dict(rot=7), dict(rot=10), dict(d=0), dict(d=1025), dict(layout=2), dict(hq=-1), dict(n=-1), dict(q=None),
                dict(freqs=None), dict(eps=-1.0), dict(factor=math.inf)):
         assert rope(**kw) == 1, kw
