@@ -23,8 +23,15 @@
 // S_w(j) becoming full implies that O_w holds block j-1's product (the MMAs of a CTA complete
 // in order), so a softmax thread may rescale its row of O_w without another barrier.
 //
-// Bound by the exponentials and the tensor core in about equal parts: a block of 128 keys and
-// two tiles of 128 rows is 4 MMAs of 512 cycles and 32768 exponentials at 16 a cycle.
+// What bounds it (16 x 2048 tokens, 32 heads of 128, timers in the roles): a tile's chain of
+// softmax (about 1700 cycles per 128 keys: 1024 of exponentials at 16 a cycle and SM, the rest issue
+// and latency), two MMA groups of 512 and the hand-overs between them (about 600), which the
+// other tile fills only in part: 3400 cycles per block and pair of tiles, of which the tensor
+// core works 2048.  Tried and slower, full attention at that size against 1.09 ms: blocks of 64
+// keys with two S per tile, so that QK runs two blocks ahead (1.42, the MMA warp's waits double);
+// P handed over in halves (1.24 to 1.36, the MMA warp then waits on one tile while the other is
+// ready); one MMA warp per tile with 32 keys at a time (1.31); more exponentials on the FMA pipe
+// than one pair in eight (1.13 at two, 1.19 at three).
 //
 // Every wait is bounded: one that runs out records PWP_ETIMEOUT and the rows come out NaN;
 // copies and MMAs in flight are waited for before a CTA leaves.
@@ -40,6 +47,7 @@ typedef __nv_bfloat16 bf16;
 constexpr int BOX = 128 * 128;                 // 128 rows of 64 bf16
 constexpr int KEYS = 128;
 constexpr int kThreadsAtt = 384;
+constexpr int kPolyPairs = 1;                      // of 8 pairs of exponentials, on the FMA pipe
 constexpr int kFlags = 8;                      // items a fixer can be ahead of an epilogue, at least
 
 template <int D>
@@ -139,9 +147,8 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 // The MMAs of one tile product are issued by one elected lane of a converged warp, in one
-// statement with the operands advanced inside it: the descriptors then stay in the uniform
-// registers the instruction takes them from.  (One asm statement per MMA under a lane test
-// took 75 cycles of issue each, more than the MMA itself.)
+// statement with the operands advanced inside it (measured in this kernel: a statement per MMA
+// costs 0.1 ms more; under a lane test with descriptors formed in between, 0.2 ms).
 //
 // S (128 x 128) = Q (128 x 64 BOXES) K^T: steps of 16 are 32 bytes inside a swizzled row, a box of
 // 64 further on after four.
@@ -237,11 +244,60 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Two fp32 operations in one instruction.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 2^x of two values on the FMA pipe: x = n + f with n the nearest whole number, f in [-1/2, 1/2],
+// and 2^f by the cubic 1 + f (a + f (b + f c)) of least largest relative error (found by linear
+// programming over 4001 points: 1.02e-4 = 2^-13.3, a sixteenth of a bf16 half step).  The
+// constant term is exactly 1, so x clamped at -127 gives exactly 0 (1's exponent field of 127,
+// less 127).
+__device__ __forceinline__ float2 exp2_poly(float2 x) {
+  const f32x2 big = pair(12582912.f, 12582912.f);      // 1.5 * 2^23: the sum's low bits are n
+  const f32x2 v = pair(fmaxf(x.x, -127.f), fmaxf(x.y, -127.f));
+  const f32x2 t = add2(v, big);
+  const f32x2 n = add2(t, pair(-12582912.f, -12582912.f));
+  const f32x2 f = fma2(n, pair(-1.f, -1.f), v);
+  f32x2 p = fma2(f, pair(0.05500893294811249f, 0.05500893294811249f), pair(0.2422109693288803f, 0.2422109693288803f));
+  p = fma2(p, f, pair(0.6932829022407532f, 0.6932829022407532f));
+  p = fma2(p, f, pair(1.f, 1.f));
+  const float2 pf = unpair(p), tf = unpair(t);
+  return make_float2(__int_as_float(__float_as_int(pf.x) + (__float_as_int(tf.x) << 23)),
+                     __int_as_float(__float_as_int(pf.y) + (__float_as_int(tf.y) << 23)));
+}
 // maximum of three, NaN if any is
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+__device__ __forceinline__ float max_of(const float* s) {
+  float m[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+  for (int i = 4; i + 8 <= KEYS; i += 8) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) m[q] = max3(m[q], s[i + 2 * q], s[i + 2 * q + 1]);
+  }
+  return max3(max3(m[0], m[1], m[2]), max3(m[3], s[KEYS - 4], s[KEYS - 3]), max3(s[KEYS - 2], s[KEYS - 1], s[KEYS - 1]));
 }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -305,7 +361,11 @@ __global__ void __launch_bounds__(kThreadsAtt, 1)
   Item x;
   bool bad = false;
 
-  if (warp == 0) {
+  // Registers: the softmax warps hold a row of 128 scores.  The CTA was launched with 384 * 168;
+  // 128 * 72 + 256 * 216 is exactly that.
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0) {
     // ---------------------------------------------------------------- copies
     uint32_t r = 0, qn[2] = {0, 0};       // slots filled, q tiles loaded
     bool ok = true;
@@ -473,8 +533,10 @@ __global__ void __launch_bounds__(kThreadsAtt, 1)
       r += 2 * (uint32_t)nb;
       ++item;
     }
+  }
   } else {
     // ---------------------------------------------------------------- softmax and output
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int w = (warp - 4) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const int tok_in = row / a.group, head_in = row - tok_in * a.group;
@@ -514,52 +576,52 @@ __global__ void __launch_bounds__(kThreadsAtt, 1)
           for (int i = 0; i < KEYS; ++i)
             if (i >= vis) s[i] = -INFINITY;
         }
-        float mx0 = max3(m, s[0], s[1]), mx1 = s[2];
+        if (j == 0) m = max_of(s);
+        // The probabilities are formed against the reference of the blocks before, and this
+        // block's maximum beside them; only when it has left the reference by more than 8 in
+        // the exponent are o and the sum rescaled and the probabilities formed again.
+        f32x2 sum2[2];
+        while (true) {
+          const f32x2 c2 = pair(a.c, a.c), mc2 = pair(-m * a.c, -m * a.c);
+          float mx4[4] = {m, m, m, m};
+          sum2[0] = sum2[1] = pair(0.f, 0.f);
 #pragma unroll
-        for (int i = 3; i + 3 < KEYS; i += 4) {
-          mx0 = max3(mx0, s[i], s[i + 1]);
-          mx1 = max3(mx1, s[i + 2], s[i + 3]);
-        }
-        const float mx = max3(mx0, mx1, s[KEYS - 1]);
-        // the reference moves when the maximum has left it by more than 8 in the exponent
-        const bool move = mine && !((mx - m) * a.c <= 8.f);
-        if (__any_sync(0xffffffffu, move)) {
-          const float fix = move ? ex2((m - mx) * a.c) : 1.f;
-          if (j > 0) {
-#pragma unroll 1
-            for (int ch = 0; ch < D; ch += 16) {
-              float o[16];
-              tmem_ld16(myO + ch, o);
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t p[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= fix;
-              tmem_st16(myO + ch, reinterpret_cast<const uint32_t*>(o));
+            for (int i = 0; i < 16; ++i) {
+              const float s0 = s[32 * ch + 2 * i], s1 = s[32 * ch + 2 * i + 1];
+              mx4[i & 3] = max3(mx4[i & 3], s0, s1);
+              const float2 e = unpair(fma2(pair(s0, s1), c2, mc2));
+              const float2 v = (i & 7) < kPolyPairs ? exp2_poly(e) : make_float2(ex2(e.x), ex2(e.y));
+              sum2[i & 1] = add2(sum2[i & 1], pair(v.x, v.y));
+              p[i] = pack2(v.x, v.y);
             }
+            tmem_st16(myS + 16 * ch, p);
+          }
+          const float mx = max3(max3(mx4[0], mx4[1], mx4[2]), mx4[3], mx4[3]);
+          const bool move = mine && !((mx - m) * a.c <= 8.f) && m == m;
+          if (!__any_sync(0xffffffffu, move)) break;
+          const float fix = move ? ex2((m - mx) * a.c) : 1.f;
+#pragma unroll 1
+          for (int ch = 0; ch < D; ch += 16) {
+            float o[16];
+            tmem_ld16(myO + ch, o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= fix;
+            tmem_st16(myO + ch, reinterpret_cast<const uint32_t*>(o));
           }
           if (move) {
-            l = j > 0 ? l * fix : 0.f;
+            l *= fix;
             m = mx;
           }
         }
-        const float mc = m * a.c;
-        float l1 = 0.f;
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          uint32_t p[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float p0 = ex2(fmaf(s[32 * ch + 2 * i], a.c, -mc));
-            const float p1 = ex2(fmaf(s[32 * ch + 2 * i + 1], a.c, -mc));
-            l += p0;
-            l1 += p1;
-            p[i] = pack2(p0, p1);
-          }
-          tmem_st16(myS + 16 * ch, p);
-        }
-        l += l1;
         tmem_wait_st();
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sb.pfull[w]);
+        const float2 l2 = unpair(add2(sum2[0], sum2[1]));
+        l += l2.x + l2.y;
       }
       if (nb > 0) {
         if (ok) {
