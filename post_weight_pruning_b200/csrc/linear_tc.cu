@@ -13,8 +13,10 @@
 //
 // skinny_kernel, for few rows, where the weights' bytes bound the time: the roles are swapped
 // (128 rows of W are the M side, up to 256 rows of x the N side, padded to 16), k is split
-// over the CTAs of a cluster so that every SM streams weights, and the partial sums are
-// added through distributed shared memory in rank order -- no atomics, no workspace.
+// over the CTAs of a cluster so that every SM streams weights.  Each CTA then stores its
+// partial sums straight from tensor memory into the shared memory of the CTA that finishes
+// those rows (stores do not wait for the other side, loads from it would), which adds them
+// in rank order -- no atomics, no workspace.  A row of 4096 x 4096 weights: MEASURED_SKINNY.
 //
 // Accumulators are fp32; bias, activation, product and residual are applied in fp32 and the
 // result is rounded to bf16 once.  Every wait is bounded: a wait that runs out records
@@ -50,10 +52,8 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
 __device__ __forceinline__ void remote_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ float2 remote_load2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void remote_store(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 // A tile load of a CTA pair: into this CTA's shared memory, counted by the barrier at `bar`
 // (a cluster address: the leader's).
@@ -368,7 +368,64 @@ struct Skinny {
   int rows, n, nk;
   int npad;            // rows of x per tile, a multiple of 16 (the tile's tensor-memory columns)
   int row_tiles, split, stages, tmem_cols;
+  int f;               // output columns per tile: rows of W, and for the gated product of W_up
 };
+
+// Adds the ranks' partial sums, part[q][row][feature], of `rows` rows and writes them: a warp per
+// row, VW neighbouring columns a lane.  Branch-free over the ranks (those past the last read its
+// sums again and add nothing).
+template <bool GATED, int ACT>
+__device__ __forceinline__ void finish_rows(const Skinny& g, const Epilogue& ep, const float* part, int per, int row0,
+                                            int rows, int c0, int warp, int lane) {
+  constexpr int VW = GATED ? 2 : 4;
+  const int f = VW * lane, c = c0 + f, cols = min(min(g.f - f, VW), g.n - c);
+  if (cols <= 0) return;
+  float b[VW], bu[VW];
+#pragma unroll
+  for (int i = 0; i < VW; ++i) {
+    b[i] = ep.bias && i < cols ? to_f32(ep.bias[c + i]) : 0.f;
+    bu[i] = GATED && ep.bias_up && i < cols ? to_f32(ep.bias_up[c + i]) : 0.f;
+  }
+  const bool whole = cols == VW;
+  for (int t = warp; t < rows; t += S_THREADS / 32) {
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};      // four columns, or two of each product
+#pragma unroll
+    for (int q = 0; q < S_MAX_CLUSTER; ++q) {
+      const float* src = part + (min(q, g.split - 1) * per + t) * S_FEATURES + f;
+      float4 x;
+      if (GATED) {
+        const float2 x0 = *reinterpret_cast<const float2*>(src), x1 = *reinterpret_cast<const float2*>(src + 64);
+        x = make_float4(x0.x, x0.y, x1.x, x1.y);
+      } else {
+        x = *reinterpret_cast<const float4*>(src);
+      }
+      sum[0] += q < g.split ? x.x : 0.f;
+      sum[1] += q < g.split ? x.y : 0.f;
+      sum[2] += q < g.split ? x.z : 0.f;
+      sum[3] += q < g.split ? x.w : 0.f;
+    }
+    const long long r = row0 + t;
+    const bf16* res = ep.residual ? ep.residual + r * ep.residual_stride + c : nullptr;
+    bf16* o = ep.out + r * ep.out_stride + c;
+    float v[VW];
+#pragma unroll
+    for (int i = 0; i < VW; ++i) {
+      v[i] = activate(ACT, sum[i] + b[i]);
+      if (GATED) v[i] *= sum[2 + (i & 1)] + bu[i];
+      if (res && i < cols) v[i] += to_f32(res[i]);
+    }
+    if (whole && ((uintptr_t)o & (2 * VW - 1)) == 0) {
+      if (GATED)
+        *reinterpret_cast<uint32_t*>(o) = pack2(v[0], v[1]);
+      else
+        *reinterpret_cast<uint2*>(o) = make_uint2(pack2(v[0], v[1]), pack2(v[VW - 2], v[VW - 1]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < VW; ++i)
+        if (i < cols) o[i] = from_f32<bf16>(v[i]);
+    }
+  }
+}
 
 template <bool GATED>
 __global__ void __launch_bounds__(S_THREADS, 1)
@@ -382,13 +439,26 @@ __global__ void __launch_bounds__(S_THREADS, 1)
   __shared__ int abort_flag;
   volatile int* abortp = &abort_flag;
 
-  constexpr int F = GATED ? S_FEATURES / 2 : S_FEATURES;   // output columns of a tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)(blockIdx.x % g.split), tile = (int)(blockIdx.x / g.split);
-  const int c0 = (tile / g.row_tiles) * F, r0 = (tile % g.row_tiles) * g.npad;
+  const int c0 = (tile / g.row_tiles) * g.f, r0 = (tile % g.row_tiles) * g.npad;
   const int kt0 = (int)((long long)g.nk * rank / g.split), kt1 = (int)((long long)g.nk * (rank + 1) / g.split);
   const int stage_bytes = (S_FEATURES + g.npad) * ROW_BYTES;
 
+  // The copies start before tensor memory is there: thread 0 sets up the barriers that they
+  // need and fills the ring.
+  // The tiles of a column of CTAs all read the same rows of x; each starts at another place of
+  // its range of k, or they would queue for the same lines of L2 at every step.
+  const int range = kt1 - kt0, turn = (int)((unsigned)tile * 37u % (unsigned)range);
+  int issued = 0;
+  auto load = [&](int i, int s) {
+    const int kt = kt0 + (i + turn < range ? i + turn : i + turn - range);
+    mbar_expect_tx(&full[s], (uint32_t)(((GATED ? 2 : 1) * g.f + g.npad) * ROW_BYTES));
+    uint8_t* a = smem + s * stage_bytes;
+    tma_load_2d(a, &wmap, &full[s], kt * TK, c0);
+    if (GATED) tma_load_2d(a + 64 * ROW_BYTES, &umap, &full[s], kt * TK, c0);
+    tma_load_2d(a + S_FEATURES * ROW_BYTES, &xmap, &full[s], kt * TK, r0);
+  };
   if (threadIdx.x == 0) {
     for (int s = 0; s < g.stages; ++s) {
       mbar_init(&full[s], 1);
@@ -397,6 +467,8 @@ __global__ void __launch_bounds__(S_THREADS, 1)
     mbar_init(&done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     abort_flag = 0;
+    pdl_wait();
+    for (; issued < g.stages && issued < range; ++issued) load(issued, issued);
   }
   if (warp == 1) tmem_alloc(&tmem_slot, (uint32_t)g.tmem_cols);
   fence_before();
@@ -407,18 +479,13 @@ __global__ void __launch_bounds__(S_THREADS, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      int issued = 0;
-      for (int kt = kt0; kt < kt1; ++kt, ++issued) {
+      for (; issued < range; ++issued) {
         const int s = issued % g.stages;
-        if (issued >= g.stages && !mbar_wait(&empty[s], (uint32_t)(issued / g.stages - 1) & 1, abortp, spin)) {
+        if (!mbar_wait(&empty[s], (uint32_t)(issued / g.stages - 1) & 1, abortp, spin)) {
           *abortp = 1;
           break;
         }
-        mbar_expect_tx(&full[s], (uint32_t)stage_bytes);
-        uint8_t* a = smem + s * stage_bytes;
-        tma_load_2d(a, &wmap, &full[s], kt * TK, c0);
-        tma_load_2d(a + 64 * ROW_BYTES, GATED ? &umap : &wmap, &full[s], kt * TK, GATED ? c0 : c0 + 64);
-        tma_load_2d(a + S_FEATURES * ROW_BYTES, &xmap, &full[s], kt * TK, r0);
+        load(issued, s);
       }
       for (int i = issued > g.stages ? issued - g.stages : 0; i < issued; ++i)
         mbar_wait(&full[i % g.stages], (uint32_t)(i / g.stages) & 1, kDrainLimit);
@@ -449,75 +516,57 @@ __global__ void __launch_bounds__(S_THREADS, 1)
   }
   fence_before();
   __syncthreads();      // every copy has landed, every MMA has finished: the stages are free
+  if (g.split > 1) cluster_sync();      // in every CTA of the cluster
   fence_after();
 
-  // This CTA's partial sums, [row of x][feature], lane = feature: consecutive addresses.
+  // Row t of the tile is finished by CTA t / per, which gets the partial sums of rank q at
+  // part[q][t % per][feature]; lane = feature, so a warp stores 128 consecutive bytes.
   const bool failed_tile = *abortp != 0;
   float* part = reinterpret_cast<float*>(smem);
+  const int have = min(g.npad, g.rows - r0);
+  int per = (have + g.split - 1) / g.split;
+  if (per > 16) per = (per + 15) & ~15;      // 16 rows read at once then go to one CTA
   const int quarter = warp & 3;
-  for (int j = (warp >> 2) * 16; j < g.npad; j += 32) {
+  const uint32_t pbase = smem_u32(part) + (uint32_t)(rank * per * S_FEATURES + quarter * 32 + lane) * 4u;
+  for (int j = (warp >> 2) * 16; j < have; j += 32) {
     float v[16];
     tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)j, v);
+    if (failed_tile) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      part[(j + i) * S_FEATURES + quarter * 32 + lane] = failed_tile ? __int_as_float(0x7fc00000) : v[i];
+      for (int i = 0; i < 16; ++i) v[i] = __int_as_float(0x7fc00000);
+    }
+    int to = j / per, at = j - to * per;
+    if (at + 16 <= per && j + 16 <= have) {
+      const uint32_t dst = map_rank(pbase + (uint32_t)(at * S_FEATURES) * 4u, (uint32_t)to);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) remote_store(dst + i * S_FEATURES * 4u, v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (j + i < have) remote_store(map_rank(pbase + (uint32_t)(at * S_FEATURES) * 4u, (uint32_t)to), v[i]);
+        if (++at == per) {
+          at = 0;
+          ++to;
+        }
+      }
+    }
   }
   if (failed_tile && threadIdx.x == 0 && st) set_error(st, PWP_ETIMEOUT, kSiteLinear);
   fence_before();
   __syncthreads();
   if (warp == 1) tmem_free(tmem, (uint32_t)g.tmem_cols);
-  if (g.split > 1) cluster_sync();
+  if (g.split > 1) cluster_sync();      // the others' sums are here
 
-  // Rank r of the cluster finishes its share of the tile's outputs, two columns a thread.
-  const int have = min(g.npad, g.rows - r0), pairs = have * (F / 2);
-  const int e0 = (int)((long long)pairs * rank / g.split), e1 = (int)((long long)pairs * (rank + 1) / g.split);
-  const uint32_t pbase = smem_u32(part);
-  for (int e = e0 + threadIdx.x; e < e1; e += S_THREADS) {
-    const int t = e / (F / 2), f = 2 * (e % (F / 2)), c = c0 + f;
-    if (c >= g.n) continue;
-    const uint32_t at = pbase + (uint32_t)(t * S_FEATURES + f) * 4u;
-    float2 v = make_float2(0.f, 0.f), u = v;
-    for (int q = 0; q < g.split; ++q) {
-      const uint32_t from = g.split > 1 ? map_rank(at, (uint32_t)q) : at;
-      const float2 p = remote_load2(from);
-      v.x += p.x;
-      v.y += p.y;
-      if (GATED) {
-        const float2 pu = remote_load2(from + 64 * 4);
-        u.x += pu.x;
-        u.y += pu.y;
-      }
-    }
-    const bool two = c + 1 < g.n;
-    if (ep.bias) {
-      v.x += to_f32(ep.bias[c]);
-      if (two) v.y += to_f32(ep.bias[c + 1]);
-    }
-    v.x = activate(ep.act, v.x);
-    v.y = activate(ep.act, v.y);
-    if (GATED) {
-      if (ep.bias_up) {
-        u.x += to_f32(ep.bias_up[c]);
-        if (two) u.y += to_f32(ep.bias_up[c + 1]);
-      }
-      v.x *= u.x;
-      v.y *= u.y;
-    }
-    const long long r = r0 + t;
-    if (ep.residual) {
-      const bf16* p = ep.residual + r * ep.residual_stride + c;
-      v.x += to_f32(p[0]);
-      if (two) v.y += to_f32(p[1]);
-    }
-    bf16* o = ep.out + r * ep.out_stride + c;
-    if (two && ((uintptr_t)o & 3) == 0) {
-      *reinterpret_cast<uint32_t*>(o) = pack2(v.x, v.y);
-    } else {
-      o[0] = from_f32<bf16>(v.x);
-      if (two) o[1] = from_f32<bf16>(v.y);
-    }
+  // one loop per activation: a branch per value costs more than everything else here
+  const int t0 = rank * per, mine = min(per, have - t0);
+  const float* from = part;
+  switch (ep.act) {
+    case PWP_ACT_RELU: finish_rows<GATED, PWP_ACT_RELU>(g, ep, from, per, r0 + t0, mine, c0, warp, lane); break;
+    case PWP_ACT_SILU: finish_rows<GATED, PWP_ACT_SILU>(g, ep, from, per, r0 + t0, mine, c0, warp, lane); break;
+    case PWP_ACT_GELU: finish_rows<GATED, PWP_ACT_GELU>(g, ep, from, per, r0 + t0, mine, c0, warp, lane); break;
+    case PWP_ACT_GELU_TANH: finish_rows<GATED, PWP_ACT_GELU_TANH>(g, ep, from, per, r0 + t0, mine, c0, warp, lane); break;
+    default: finish_rows<GATED, PWP_ACT_NONE>(g, ep, from, per, r0 + t0, mine, c0, warp, lane); break;
   }
-  if (g.split > 1) cluster_sync();      // the others have read this CTA's sums
 }
 
 // ---------------------------------------------------------------- host side
@@ -561,8 +610,44 @@ cudaError_t run_pair(const pwp_linear_args& a, const Epilogue& ep, cudaStream_t 
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
+// How many CTAs of the skinny kernel run at once in clusters of c, one to an SM: all SMs less
+// what clusters leave over in a group of SMs.  (The query counts one CTA of a kernel that
+// holds tensor memory per SM; two run beside each other when their shared memory fits.)
+template <bool GATED>
+int resident_ctas(int c) {
+  static std::atomic<int> known[64][S_MAX_CLUSTER + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev][c].load();
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(c * kNumSM));
+    cfg.blockDim = dim3(S_THREADS);
+    cfg.dynamicSmemBytes = 225 * 1024;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, skinny_kernel<GATED>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    n = clusters * c;
+    known[dev][c].store(n);
+  }
+  return n;
+}
+
 template <bool GATED>
 cudaError_t run_skinny(const pwp_linear_args& a, const Epilogue& ep, cudaStream_t s, bool* used) {
+  static std::atomic<unsigned long long> attr_done{0};
+  if (first_on_device(attr_done)) {
+    cudaError_t e = cudaFuncSetAttribute(skinny_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+    if (e != cudaSuccess) return e;
+  }
   constexpr int F = GATED ? S_FEATURES / 2 : S_FEATURES;
   Skinny g;
   g.rows = (int)a.rows;
@@ -574,32 +659,36 @@ cudaError_t run_skinny(const pwp_linear_args& a, const Epilogue& ep, cudaStream_
   g.tmem_cols = 32;
   while (g.tmem_cols < g.npad) g.tmem_cols *= 2;
   const int stage_bytes = (S_FEATURES + g.npad) * ROW_BYTES;
-  const long long tiles = (long long)((a.n + F - 1) / F) * g.row_tiles;
-  // up to 64 rows two CTAs fit an SM
+  // Up to 64 rows the stages of two CTAs fit an SM.
   const int per_sm = g.npad <= 64 ? 2 : 1;
   const int budget = (per_sm == 2 ? 112 : 224) * 1024 - 1024;
   g.stages = budget / stage_bytes < S_MAX_STAGES ? budget / stage_bytes : S_MAX_STAGES;
-  const long long slots = (long long)kNumSM * per_sm;
-  long long split = slots / tiles;
-  if (split > S_MAX_CLUSTER) split = S_MAX_CLUSTER;
-  if (split > g.nk) split = g.nk;
-  if (split < 1) split = 1;
-  g.split = (int)split;
-  if (tiles * split > 0x7fffffffLL) return cudaSuccess;
+  // The largest split whose CTAs are all resident at once: a second round of clusters costs as
+  // much as the first (601 x 4096 x 1000: 17 us split 5 ways, 29 us split 6).
+  long long tiles = (long long)((a.n + F - 1) / F) * g.row_tiles;
+  int split = 1;
+  for (int c = 2; c <= S_MAX_CLUSTER && c <= g.nk; ++c)
+    if (tiles * c <= resident_ctas<GATED>(c) * per_sm) split = c;
+  g.f = F;
+  if (split == 1 && per_sm == 2) {
+    // As many rounds of CTAs as that takes anyway, with equal shares of the columns.
+    const long long slots = kNumSM * per_sm / g.row_tiles, rounds = (tiles + slots - 1) / slots;
+    g.f = (int)((a.n + slots * rounds - 1) / (slots * rounds));
+    g.f = (g.f + 3) & ~3;
+    if (g.f > F) g.f = F;
+    tiles = (long long)((a.n + g.f - 1) / g.f) * g.row_tiles;
+  }
+  g.split = split;
+  if (tiles > 0x7fffffffLL / split) return cudaSuccess;
   int smem = g.stages * stage_bytes;
-  const int parts = g.npad * S_FEATURES * (int)sizeof(float);
+  const int parts = (g.npad + 16 * g.split) * S_FEATURES * (int)sizeof(float);
   if (smem < parts) smem = parts;
   smem += 1024;
   CUtensorMap xm, wm, um;
-  if (!make_map(&xm, a.x_dev, a.rows, a.k, a.x_stride, g.npad) || !make_map(&wm, a.w_dev, a.n, a.k, a.w_stride, 64))
+  if (!make_map(&xm, a.x_dev, a.rows, a.k, a.x_stride, g.npad) || !make_map(&wm, a.w_dev, a.n, a.k, a.w_stride, g.f))
     return cudaSuccess;
   um = wm;
-  if (GATED && !make_map(&um, a.w_up_dev, a.n, a.k, a.w_up_stride, 64)) return cudaSuccess;
-  static std::atomic<unsigned long long> attr_done{0};
-  if (first_on_device(attr_done)) {
-    cudaError_t e = cudaFuncSetAttribute(skinny_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
-    if (e != cudaSuccess) return e;
-  }
+  if (GATED && !make_map(&um, a.w_up_dev, a.n, a.k, a.w_up_stride, g.f)) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * split));
   cfg.blockDim = dim3(S_THREADS);
