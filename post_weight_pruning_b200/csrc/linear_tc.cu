@@ -71,6 +71,11 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
           smem_u32(bar))
       : "memory");
 }
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.b32 %0, 1, 0, q;\n\t}" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -94,6 +99,7 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n) {
 // ---------------------------------------------------------------- epilogue pieces
 
 struct Epilogue {
+  int vec;             // rows of out and residual can be read and written 16 bytes at a time
   const bf16* bias;
   const bf16* bias_up;
   const bf16* residual;
@@ -170,10 +176,11 @@ __device__ __forceinline__ void activate32(int act, float (&v)[32]) {
 // ---------------------------------------------------------------- many rows
 
 constexpr int P_ROWS = 128;                       // rows of x, and of W, per CTA
-constexpr int P_STAGES = 7;
+constexpr int P_STAGES = 6;
 constexpr int P_STAGE_BYTES = 2 * P_ROWS * ROW_BYTES;   // 32 KB
-constexpr int P_SMEM = P_STAGES * P_STAGE_BYTES + 1024 + 256;
-constexpr int P_EPI_WARPS = 4, P_THREADS = 32 * (2 + P_EPI_WARPS);
+constexpr int P_EPI_WARPS = 8, P_THREADS = 32 * (2 + P_EPI_WARPS);
+constexpr int P_TURN = 32 * 128;                        // a warp's 32 rows of 64 bf16, for its output
+constexpr int P_SMEM = P_STAGES * P_STAGE_BYTES + P_EPI_WARPS * P_TURN + 1024 + 256;
 constexpr int P_ACC_COLS = 256;
 constexpr int P_GROUP = 8;                        // row tiles that share W tiles while they are in L2
 
@@ -193,7 +200,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
                 long long spin) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + P_STAGES * P_STAGE_BYTES);   // the leader's are used
+  uint8_t* turn_all = smem + P_STAGES * P_STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(turn_all + P_EPI_WARPS * P_TURN);   // the leader's are used
   uint64_t* empty = full + P_STAGES;
   uint64_t* afull = empty + P_STAGES;
   uint64_t* aempty = afull + 2;                                                    // the leader's are used
@@ -239,7 +247,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
       prefetch_map(&xmap);
       prefetch_map(&wmap);
       const uint32_t sbase = smem_u32(smem);
-      long long it = 0;
+      const uint32_t bar0 = map_rank(smem_u32(&full[0]), 0);
+      uint32_t s = 0, phase = 0, filled = 0;      // next stage, its phase; stages ever filled (capped)
       bool ok = true;
       for (int t = first; t < tiles && ok; t += pairs) {
         int m, c;
@@ -247,31 +256,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
         const int y = m * 2 * P_ROWS + (int)rank * P_ROWS;
         const CUtensorMap* bmap = GATED && rank ? &umap : &wmap;
         const int yb = GATED ? c * NT : c * NT + (int)rank * P_ROWS;
-        for (int kt = 0; kt < nk; ++kt, ++it) {
-          const int s = (int)(it % P_STAGES);
-          if (it >= P_STAGES && !mbar_wait(&empty[s], (uint32_t)((it / P_STAGES) - 1) & 1, abortp, spin)) {
+        for (int kt = 0; kt < nk; ++kt) {
+          if (filled < P_STAGES) {
+            ++filled;
+          } else if (!mbar_wait(&empty[s], phase ^ 1u, abortp, spin)) {
             ok = false;
             break;
           }
-          const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
           if (rank == 0) mbar_expect_tx(&full[s], 2 * P_STAGE_BYTES);
-          const uint32_t dst = sbase + s * P_STAGE_BYTES;
+          const uint32_t dst = sbase + s * P_STAGE_BYTES, bar = bar0 + s * 8u;
           tma_load_pair(dst, &xmap, bar, kt * TK, y);
           tma_load_pair(dst + P_ROWS * ROW_BYTES, bmap, bar, kt * TK, yb);
+          if (++s == P_STAGES) {
+            s = 0;
+            phase ^= 1u;
+          }
         }
       }
       if (!ok) *abortp = 1;
       // both CTAs' copies land before either leaves: they are counted by the leader's barriers
       if (rank == 0)
-        for (long long i = it > P_STAGES ? it - P_STAGES : 0; i < it; ++i)
-          mbar_wait(&full[i % P_STAGES], (uint32_t)(i / P_STAGES) & 1, kDrainLimit);
+        for (uint32_t i = 0; i < filled; ++i) {
+          if (s == 0) phase ^= 1u;
+          s = s == 0 ? P_STAGES - 1 : s - 1;
+          mbar_wait(&full[s], phase, kDrainLimit);
+        }
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      const uint32_t sbase = smem_u32(smem);
+    if (rank == 0 && elected()) {
+      // descriptors of stage 0; a stage, and a step of 16 along k, on are additions
+      const uint64_t da0 = sw128_desc(smem_u32(smem), 16, 1024);
+      const uint64_t db0 = sw128_desc(smem_u32(smem) + P_ROWS * ROW_BYTES, 16, 1024);
       constexpr uint32_t idesc = idesc_bf16(256, 256);
-      long long it = 0;
+      uint32_t s = 0, phase = 0;
       int i = 0;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += pairs, ++i) {
@@ -282,18 +300,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
         }
         fence_after();
         const uint32_t d = tmem + (uint32_t)(a * P_ACC_COLS);
-        for (int kt = 0; kt < nk; ++kt, ++it) {
-          const int s = (int)(it % P_STAGES);
-          if (!mbar_wait(&full[s], (uint32_t)(it / P_STAGES) & 1, abortp, spin)) {
+        for (int kt = 0; kt < nk; ++kt) {
+          if (!mbar_wait(&full[s], phase, abortp, spin)) {
             ok = false;
             break;
           }
           fence_after();
-          const uint32_t pa = sbase + s * P_STAGE_BYTES, pb = pa + P_ROWS * ROW_BYTES;
+          const uint64_t off = s * (P_STAGE_BYTES >> 4);
 #pragma unroll
-          for (int kk = 0; kk < TK / 16; ++kk)
-            mma_pair(d, sw128_desc(pa + kk * 32, 16, 1024), sw128_desc(pb + kk * 32, 16, 1024), idesc, (kt | kk) != 0);
+          for (int kk = 0; kk < TK / 16; ++kk) mma_pair(d, da0 + off + 2 * kk, db0 + off + 2 * kk, idesc, (kt | kk) != 0);
           commit_pair(&empty[s]);
+          if (++s == P_STAGES) {
+            s = 0;
+            phase ^= 1u;
+          }
         }
         if (ok) commit_pair(&afull[a]);
       }
@@ -303,7 +323,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
     }
     __syncwarp();
   } else {
-    const int quarter = warp & 3;
+    // warp e reads the tensor-memory lanes 32 (e % 4).. and half of the tile's columns
+    const int quarter = warp & 3, part = (warp - 2) >> 2;
     int i = 0;
     bool ok = true;
     for (int t = first; t < tiles; t += pairs, ++i) {
@@ -319,29 +340,89 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
       fence_after();
       int m, c;
       pair_tile(t, mt, nt, m, c);
-      const long long r = (long long)m * 2 * P_ROWS + rank * P_ROWS + quarter * 32 + lane;
+      const long long rw = (long long)m * 2 * P_ROWS + rank * P_ROWS + quarter * 32, r = rw + lane;   // warp's, thread's row
       const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(a * P_ACC_COLS);
+      uint8_t* turn = turn_all + (warp - 2) * P_TURN;
+      // 64 columns at a time.  A thread holds a row, but 32 rows' 16-byte pieces make 32 separate
+      // writes; turned through shared memory (16-byte pieces swizzled by row) a warp writes, and
+      // reads of the residual, four whole 128-byte lines.
+      const int prow = lane >> 3, pcol = lane & 7;
 #pragma unroll 1
-      for (int ch = 0; ch < NT / 32; ++ch) {
-        const int c0 = c * NT + ch * 32, avail = n - c0;
+      for (int ch = part * (NT / 128); ch < (part + 1) * (NT / 128); ++ch) {
+        const int c0 = c * NT + ch * 64, avail = n - c0;
         if (avail <= 0) break;
-        float v[32], u[32];
-        tmem_ld32(base + (uint32_t)(ch * 32), v);
-        if (GATED) tmem_ld32(base + (uint32_t)(128 + ch * 32), u);
-        if (ep.bias) add32(v, ep.bias + c0, avail);
-        activate32(ep.act, v);
-        if (GATED) {
-          if (ep.bias_up) add32(u, ep.bias_up + c0, avail);
+        const bool on = 8 * pcol < avail;
+        if (ep.vec && ep.residual) {
+          uint4 u[8];
+          const bf16* p = ep.residual + (rw + prow) * ep.residual_stride + c0 + 8 * pcol;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] *= u[j];
+          for (int i = 0; i < 8; ++i)
+            if (on && rw + prow + 4 * i < rows) u[i] = *reinterpret_cast<const uint4*>(p + 4 * i * ep.residual_stride);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int q = prow + 4 * i;
+            *reinterpret_cast<uint4*>(turn + q * 128 + ((pcol ^ (q & 7)) << 4)) = u[i];
+          }
+          __syncwarp();
         }
-        if (r < rows) {
-          if (ep.residual) add32(v, ep.residual + r * ep.residual_stride + c0, avail);
+        float acc[2][32];
+        tmem_ld32_nowait(base + (uint32_t)(ch * 64), acc[0]);
+        tmem_ld32_nowait(base + (uint32_t)((GATED ? 128 : 32) + ch * 64), acc[1]);
+        tmem_wait_ld();
+        pin32(acc[0]);
+        pin32(acc[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c1 = c0 + 32 * h, left = n - c1;
+          if (left <= 0) break;
+          if (GATED && h == 1) {
+            tmem_ld32_nowait(base + (uint32_t)(32 + ch * 64), acc[0]);
+            tmem_ld32_nowait(base + (uint32_t)(160 + ch * 64), acc[1]);
+            tmem_wait_ld();
+            pin32(acc[0]);
+            pin32(acc[1]);
+          }
+          float(&v)[32] = GATED ? acc[0] : acc[h];
+          float(&u)[32] = acc[1];
+          if (ep.bias) add32(v, ep.bias + c1, left);
+          activate32(ep.act, v);
+          if (GATED) {
+            if (ep.bias_up) add32(u, ep.bias_up + c1, left);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] *= u[j];
+          }
           if (!ok) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __int_as_float(0x7fc00000);
           }
-          store32(ep.out + r * ep.out_stride + c0, v, avail);
+          if (ep.vec) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint4* at = reinterpret_cast<uint4*>(turn + lane * 128 + (((4 * h + q) ^ (lane & 7)) << 4));
+              if (ep.residual) {
+                float w[8];
+                unpack8(*at, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[8 * q + j] += w[j];
+              }
+              *at = make_uint4(pack2(v[8 * q], v[8 * q + 1]), pack2(v[8 * q + 2], v[8 * q + 3]),
+                               pack2(v[8 * q + 4], v[8 * q + 5]), pack2(v[8 * q + 6], v[8 * q + 7]));
+            }
+          } else if (r < rows) {
+            if (ep.residual) add32(v, ep.residual + r * ep.residual_stride + c1, left);
+            store32(ep.out + r * ep.out_stride + c1, v, left);
+          }
+        }
+        if (ep.vec) {
+          __syncwarp();
+          bf16* p = ep.out + (rw + prow) * ep.out_stride + c0 + 8 * pcol;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int q = prow + 4 * i;
+            const uint4 u = *reinterpret_cast<const uint4*>(turn + q * 128 + ((pcol ^ (q & 7)) << 4));
+            if (on && rw + q < rows) *reinterpret_cast<uint4*>(p + 4 * i * ep.out_stride) = u;
+          }
+          __syncwarp();
         }
       }
       fence_before();
@@ -716,7 +797,10 @@ cudaError_t run_skinny(const pwp_linear_args& a, const Epilogue& ep, cudaStream_
 cudaError_t launch_linear_tc(const pwp_linear_args& a, cudaStream_t s, bool* used) {
   *used = false;
   if (a.type != PWP_BF16) return cudaSuccess;
-  const Epilogue ep{(const bf16*)a.bias_dev, (const bf16*)a.bias_up_dev, (const bf16*)a.residual_dev, (bf16*)a.out_dev,
+  const long long os = a.rows > 1 ? a.out_stride : 8, rs = a.rows > 1 ? a.residual_stride : 8;
+  const bool vec = (a.n & 7) == 0 && (os & 7) == 0 && ((uintptr_t)a.out_dev & 15) == 0 &&
+                   (!a.residual_dev || ((rs & 7) == 0 && ((uintptr_t)a.residual_dev & 15) == 0));
+  const Epilogue ep{vec ? 1 : 0, (const bf16*)a.bias_dev, (const bf16*)a.bias_up_dev, (const bf16*)a.residual_dev, (bf16*)a.out_dev,
                     a.residual_stride, a.out_stride, a.activation};
   const bool gated = a.w_up_dev != nullptr;
   // Too few 256-row tiles to fill the SMs' pairs: split k instead.
