@@ -11,7 +11,8 @@
 // A persistent CTA takes pairs of tiles of 128 query rows.  A tile's rows are tokens times the
 // query heads that share a key head (row = token * group + head), so grouped heads read their
 // keys once and short sequences fill tiles; one TMA box gathers them.  Roles:
-//   warp 0         TMA: q of both tiles, then K_0, V_0, K_1, V_1, ... through a ring of slots
+//   warp 0         finds the items (tile pairs), hands them to the others through a short queue,
+//                  and copies: q of both tiles, then K_0, V_0, K_1, V_1, ... through a ring
 //   warp 1         MMA: S_w = Q_w K_j^T and O_w += P_w V_j for the two tiles w in turn, so the
 //                  tensor core works on one tile while the other's softmax runs.  P_w
 //                  (bf16) overlays S_w in tensor memory and is the A operand from there.
@@ -20,18 +21,19 @@
 //                  cuts, non-finite values are zeroed and added back at the end to the rows
 //                  that do see them
 //   warps 4-7, 8-11  softmax of tile 0 and 1, one row per thread, and the rows' output
-// S_w(j) becoming full implies that O_w holds block j-1's product (the MMAs of a CTA complete
+// S_w(j) becoming full implies that O_w holds block j-1's product (the MMAs of a thread complete
 // in order), so a softmax thread may rescale its row of O_w without another barrier.
 //
-// What bounds it (16 x 2048 tokens, 32 heads of 128, timers in the roles): a tile's chain of
-// softmax (about 1700 cycles per 128 keys: 1024 of exponentials at 16 a cycle and SM, the rest issue
-// and latency), two MMA groups of 512 and the hand-overs between them (about 600), which the
-// other tile fills only in part: 3400 cycles per block and pair of tiles, of which the tensor
-// core works 2048.  Tried and slower, full attention at that size against 1.09 ms: blocks of 64
-// keys with two S per tile, so that QK runs two blocks ahead (1.42, the MMA warp's waits double);
-// P handed over in halves (1.24 to 1.36, the MMA warp then waits on one tile while the other is
-// ready); one MMA warp per tile with 32 keys at a time (1.31); more exponentials on the FMA pipe
-// than one pair in eight (1.13 at two, 1.19 at three).
+// What bounds it (16 x 2048 tokens, 32 heads of 128: 0.61 ms causal, 0.95 ms full, 895 and 1155
+// TFLOP/s): a tile's chain of softmax (about 1700 cycles per 128 keys: 1024 of exponentials at
+// 16 a cycle and SM, the rest issue and latency), its two MMA groups of 512 and the hand-overs
+// between them, which the other tile fills only in part; the tensor core works two thirds of
+// the time.  The single-thread roles are bound by instruction issue and fetch, so they hold
+// little code: running slots and descriptors and no item search were worth 0.09 ms of 0.70.
+// Tried and slower (full attention): P handed over in halves (1.24 ms, and 1.15 with an MMA warp
+// per tile); blocks of 64 keys with two S per tile (1.42); 32 keys at a time (1.31); the sum in
+// place of the maximum as the reference's guard (0.99); none (0.97) or three of eight pairs of
+// exponentials (1.19) on the FMA pipe.
 //
 // Every wait is bounded: one that runs out records PWP_ETIMEOUT and the rows come out NaN;
 // copies and MMAs in flight are waited for before a CTA leaves.
@@ -48,7 +50,7 @@ constexpr int BOX = 128 * 128;                 // 128 rows of 64 bf16
 constexpr int KEYS = 128;
 constexpr int kThreadsAtt = 384;
 constexpr int kPolyPairs = 1;                      // of 8 pairs of exponentials, on the FMA pipe
-constexpr int kFlags = 8;                      // items a fixer can be ahead of an epilogue, at least
+constexpr int kQueue = 4;                      // items handed out ahead
 
 template <int D>
 struct Cfg {
@@ -70,17 +72,20 @@ struct Att {
 };
 
 // The items of a CTA, in order: the sequences' tile pairs (the last, longest one of a
-// sequence first) with the key heads running fastest.
+// sequence first) with the key heads running fastest.  Warp 0 finds them and hands them to
+// the other roles through a short queue in shared memory.
 struct Items {
   int t, s0, base;        // next item; the first sequence of the scan's chunk; tiles before it
 };
-struct Item {
-  int begin, len, hk;     // sequence, key head
-  int tok[2];             // first token of each tile
+struct __align__(16) Item {
+  int begin, len, hk;     // sequence (len < 0: no more items), key head
+  int tok;                // first token of tile 0; tile 1 starts tq tokens on
   int nb[2];              // key blocks of each tile (0: no rows)
-  int fix;                // first block of V that the fixer looks at
+  int fix;                // first block of V that the fixers look at
+  int steps;              // key blocks of the item
 };
 
+// The next item of this CTA (whole warp); false past the last one.
 __device__ __forceinline__ bool next_item(const Att& a, Items& it, Item& x, bool& bad) {
   const int lane = threadIdx.x & 31;
   const int per = 2 * a.tq;
@@ -111,15 +116,14 @@ __device__ __forceinline__ bool next_item(const Att& a, Items& it, Item& x, bool
       x.begin = __shfl_sync(0xffffffffu, b, l);
       x.len = __shfl_sync(0xffffffffu, len, l);
       const int after = __shfl_sync(0xffffffffu, sum, l);      // tiles up to and with this sequence's
-      const int p = it.base + after - 1 - tile;                // its tiles from the last one
-      x.tok[0] = p * per;
-      x.tok[1] = x.tok[0] + a.tq;
+      x.tok = (it.base + after - 1 - tile) * per;              // its tiles from the last one
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        const int last = min(x.len, x.tok[w] + a.tq);
-        x.nb[w] = x.tok[w] >= x.len ? 0 : ((a.causal ? last : x.len) + KEYS - 1) / KEYS;
+        const int first = x.tok + w * a.tq;
+        x.nb[w] = first >= x.len ? 0 : ((a.causal ? min(x.len, first + a.tq) : x.len) + KEYS - 1) / KEYS;
       }
-      x.fix = a.causal ? (x.tok[0] + 1) / KEYS : x.len / KEYS;
+      x.fix = a.causal ? (x.tok + 1) / KEYS : x.len / KEYS;
+      x.steps = max(x.nb[0], x.nb[1]);
       return true;
     }
     if (broken) {
@@ -146,64 +150,53 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
-// The MMAs of one tile product are issued by one elected lane of a converged warp, in one
-// statement with the operands advanced inside it (measured in this kernel: a statement per MMA
-// costs 0.1 ms more; under a lane test with descriptors formed in between, 0.2 ms).
-//
-// S (128 x 128) = Q (128 x 64 BOXES) K^T: steps of 16 are 32 bytes inside a swizzled row, a box of
-// 64 further on after four.
-template <int BOXES>
-__device__ __forceinline__ void mma_qk(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc) {
+// MMAs of one tile product, issued by one thread: descriptors are a base plus constants.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred q, f, t;\n\t.reg .b64 x, y;\n\t"
-      "setp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
-      "add.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-      "add.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-      "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t}" ::"r"(d),
-      "l"(da), "l"(db), "r"(idesc)
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(da), "l"(db), "r"(idesc), "r"(acc)
       : "memory");
-  if (BOXES == 2)
-    asm volatile(
-        "{\n\t.reg .pred q, t;\n\t.reg .b64 x, y;\n\t"
-        "setp.eq.b32 t, 0, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
-        "add.s64 x, %1, 1024;\n\tadd.s64 y, %2, 1024;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-        "add.s64 x, %1, 1026;\n\tadd.s64 y, %2, 1026;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-        "add.s64 x, %1, 1028;\n\tadd.s64 y, %2, 1028;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-        "add.s64 x, %1, 1030;\n\tadd.s64 y, %2, 1030;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t}" ::"r"(d),
-        "l"(da), "l"(db), "r"(idesc)
-        : "memory");
 }
-// O += P V over 64 keys: P in tensor memory (16 keys are 8 columns), V MN-major (16 keys are
-// 2048 bytes).
-__device__ __forceinline__ void mma_pv64(uint32_t d, uint32_t ta, uint64_t db, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t ta, uint64_t db, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred q, p, t;\n\t.reg .b64 y;\n\t.reg .b32 a;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-      "add.s32 a, %1, 8;\n\tadd.s64 y, %2, 128;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %3, t;\n\t"
-      "add.s32 a, %1, 16;\n\tadd.s64 y, %2, 256;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %3, t;\n\t"
-      "add.s32 a, %1, 24;\n\tadd.s64 y, %2, 384;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %3, t;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(ta), "l"(db), "r"(idesc), "r"(acc)
       : "memory");
 }
-// One arrival on `bar` when the MMAs issued so far have completed (the whole warp calls it).
-__device__ __forceinline__ void commit_elected(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
-      : "memory");
+// S (128 x 128) = Q (128 x 64 BOXES) K^T: steps of 16 are 32 bytes inside a swizzled row, a box of
+// 64 further on after four.
+template <int BOXES>
+__device__ __forceinline__ void mma_qk(uint32_t d, uint64_t dq, uint64_t dk, uint32_t idesc) {
+#pragma unroll
+  for (int i = 0; i < 4 * BOXES; ++i) {
+    const uint32_t off = (i / 4) * (BOX >> 4) + (i % 4) * 2;
+    mma_ss(d, dq + off, dk + off, idesc, i != 0);
+  }
 }
+// O += P V over 128 keys: P in tensor memory (16 keys are 8 columns), V MN-major (16 keys are
+// 2048 bytes).
+__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t p, uint64_t dv, uint32_t idesc, uint32_t acc) {
+#pragma unroll
+  for (int i = 0; i < KEYS / 16; ++i) mma_ts(d, p + 8 * i, dv + i * 128, idesc, i != 0 ? 1u : acc);
+}
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.b32 %0, 1, 0, q;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// Position in a ring of N slots: the slot, and the phase of its barriers.
+template <uint32_t N>
+struct Ring {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
 // A wait the whole warp takes part in; every lane gets the same answer.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort, long long limit) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit));
@@ -291,7 +284,9 @@ struct Bars {
   uint64_t full[8], empty[8], fixed[8];        // ring slots
   uint64_t qfull[2], qempty[2], sfull[2], pfull[2], ofull[2], oempty[2];
   uint64_t drain;
-  int vbad[kFlags];                            // item + 1: a non-finite value was taken out of its V
+  uint64_t ifull[kQueue], iempty[kQueue];
+  Item item[kQueue];
+  int vbad[kQueue];                            // item + 1: a non-finite value was taken out of its V
   int abort_flag;
   uint32_t tmem;
 };
@@ -325,7 +320,11 @@ __global__ void __launch_bounds__(kThreadsAtt, 1)
     mbar_init(&sb.drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     sb.abort_flag = 0;
-    for (int i = 0; i < kFlags; ++i) sb.vbad[i] = 0;
+    for (int i = 0; i < kQueue; ++i) {
+      mbar_init(&sb.ifull[i], 1);
+      mbar_init(&sb.iempty[i], 11);     // the MMA warp, the fixers and the softmax warps
+      sb.vbad[i] = 0;
+    }
   }
   if (warp == 1) tmem_alloc(&sb.tmem, 512);
   fence_before();
@@ -335,210 +334,236 @@ __global__ void __launch_bounds__(kThreadsAtt, 1)
   const uint32_t tmem = sb.tmem;
   const uint32_t tS = tmem, tO = tmem + 256;      // S_w at 128 w, O_w at 256 + 128 w
 
-  Items it{(int)blockIdx.x, 0, 0};
-  Item x;
-  bool bad = false;
-
   // Registers: the softmax warps hold a row of 128 scores.  The CTA was launched with 384 * 168;
-  // 128 * 72 + 256 * 216 is exactly that.
+  // 128 * 88 + 256 * 208 is exactly that.
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {
-    // ---------------------------------------------------------------- copies
-    uint32_t r = 0, qn[2] = {0, 0};       // slots filled, q tiles loaded
-    bool ok = true;
+    // ---------------------------------------------------------------- items and copies
+    Items it{(int)blockIdx.x, 0, 0};
+    Ring<C::SLOTS> rg;
+    Ring<kQueue> iq;
+    uint32_t filled = 0, items = 0, qn[2] = {0, 0};       // slots ever filled (capped), items, q tiles so far
+    bool ok = true, more = true, bad = false;
     const uint32_t qbytes = (uint32_t)(C::BOXES * a.tq * a.group * 128);
-    while (ok && next_item(a, it, x, bad)) {
-      if (lane == 0) {
-        const int nb = max(x.nb[0], x.nb[1]);
-        for (int j = 0; j < nb && ok; ++j) {
-          if (j == 0) {
-            for (int w = 0; w < 2 && ok; ++w) {
-              if (!x.nb[w]) continue;
-              if (qn[w] && !mbar_wait(&sb.qempty[w], (qn[w] - 1) & 1, abortp, spin)) {
-                ok = false;
-                break;
-              }
-              mbar_expect_tx(&sb.qfull[w], qbytes);
-              for (int b = 0; b < C::BOXES; ++b)
-                tma_load_4d(smem + w * C::TILE + b * BOX, &qmap, &sb.qfull[w], 64 * b, 0, x.hk, x.begin + x.tok[w]);
-              ++qn[w];
-            }
-          }
-          for (int kv = 0; kv < 2 && ok; ++kv) {
-            const int s = (int)(r % C::SLOTS);
-            if (r >= C::SLOTS && !mbar_wait(&sb.empty[s], (r / C::SLOTS - 1) & 1, abortp, spin)) {
-              ok = false;
-              break;
-            }
-            mbar_expect_tx(&sb.full[s], C::TILE);
-            for (int b = 0; b < C::BOXES; ++b)
-              tma_load_3d(ring + s * C::TILE + b * BOX, kv ? &vmap : &kmap, &sb.full[s], 64 * b, x.hk, x.begin + j * KEYS);
-            ++r;
-          }
+    while (ok && more) {
+      Item x;
+      more = next_item(a, it, x, bad);
+      if (elected()) {
+        if (!more) x.len = -1;
+        if (items >= kQueue) ok = mbar_wait(&sb.iempty[iq.slot], iq.phase ^ 1u, abortp, spin);
+        if (ok) {
+          sb.item[iq.slot] = x;
+          mbar_arrive(&sb.ifull[iq.slot]);
+        }
+        for (int w = 0; w < 2 && ok && more; ++w) {
+          if (!x.nb[w]) continue;
+          if (qn[w]) ok = mbar_wait(&sb.qempty[w], (qn[w] - 1) & 1, abortp, spin);
+          if (!ok) break;
+          mbar_expect_tx(&sb.qfull[w], qbytes);
+          for (int b = 0; b < C::BOXES; ++b)
+            tma_load_4d(smem + w * C::TILE + b * BOX, &qmap, &sb.qfull[w], 64 * b, 0, x.hk, x.begin + x.tok + w * a.tq);
+          ++qn[w];
+        }
+        for (int j2 = 0; ok && more && j2 < 2 * x.steps; ++j2) {
+          if (filled < C::SLOTS)
+            ++filled;
+          else
+            ok = mbar_wait(&sb.empty[rg.slot], rg.phase ^ 1u, abortp, spin);
+          if (!ok) break;
+          mbar_expect_tx(&sb.full[rg.slot], C::TILE);
+          for (int b = 0; b < C::BOXES; ++b)
+            tma_load_3d(ring + rg.slot * C::TILE + b * BOX, (j2 & 1) ? &vmap : &kmap, &sb.full[rg.slot], 64 * b, x.hk,
+                        x.begin + (j2 >> 1) * KEYS);
+          rg.step();
         }
         if (!ok) *abortp = 1;
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ++items;
+      iq.step();
+      ok = __all_sync(0xffffffffu, ok);
     }
-    if (lane == 0) {
+    if (elected()) {
       if (bad && a.st) set_error(a.st, PWP_EINVAL, kSiteAttention);
-      for (uint32_t i = r > C::SLOTS ? r - C::SLOTS : 0; i < r; ++i)
-        mbar_wait(&sb.full[i % C::SLOTS], (i / C::SLOTS) & 1, kDrainLimit);
+      for (uint32_t i = 0; i < filled; ++i) {
+        if (rg.slot == 0) rg.phase ^= 1u;
+        rg.slot = rg.slot == 0 ? C::SLOTS - 1 : rg.slot - 1;
+        mbar_wait(&sb.full[rg.slot], rg.phase, kDrainLimit);
+      }
       for (int w = 0; w < 2; ++w)
         if (qn[w]) mbar_wait(&sb.qfull[w], (qn[w] - 1) & 1, kDrainLimit);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMAs
-    const uint32_t sq = smem_u32(smem), sr = smem_u32(ring);
+    // descriptors of slot 0 and tile 0; slots and tiles further on are additions
+    const uint64_t dq0 = sw128_desc(smem_u32(smem), 16, 1024), dk0 = sw128_desc(smem_u32(ring), 16, 1024);
+    const uint64_t dv0 = sw128_desc(smem_u32(ring), BOX, 1024);
     constexpr uint32_t id_qk = idesc_of(KEYS, 0), id_pv = idesc_of(D, 1);
-    uint32_t r = 0, fixpar = 0;
-    uint32_t nq = 0, np[2] = {0, 0}, no[2] = {0, 0};   // items, blocks and outputs so far
+    constexpr uint32_t STEP = C::TILE >> 4;
+    uint32_t slot = 0, phase = 0, fixpar = 0;       // the ring's next slot, the phase of its barriers
+    uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};   // q tiles, blocks and outputs so far
     bool ok = true;
-    while (ok && next_item(a, it, x, bad)) {
-      const int nb = max(x.nb[0], x.nb[1]);
-      // S_w(0), then for every block O_w += P_w V_j and S_w(j + 1), the tiles in turn
-      for (int j = -1; j < nb && ok; ++j) {
-        const uint32_t rk = r + 2 * (uint32_t)(j + 1), rv = rk - 1;
-        const int sk = (int)(rk % C::SLOTS), sv = (int)(rv % C::SLOTS);
-        const uint32_t kb = sr + sk * C::TILE, vb = sr + sv * C::TILE;
-        if (j >= 0) {
-          ok = warp_wait(&sb.full[sv], (rv / C::SLOTS) & 1, abortp, spin);
-          if (ok && j >= x.fix) {
-            ok = warp_wait(&sb.fixed[sv], (fixpar >> sv) & 1, abortp, spin);
-            fixpar ^= 1u << sv;
+    auto advance = [&]() {
+      if (++slot == C::SLOTS) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    };
+    if (elected()) {
+      Ring<kQueue> iq;
+      while (ok) {
+        ok = mbar_wait(&sb.ifull[iq.slot], iq.phase, abortp, spin);
+        if (!ok) break;
+        const Item x = sb.item[iq.slot];
+        if (x.len < 0) break;
+        // S_w(0), then for every block O_w += P_w V_j and S_w(j + 1), the tiles in turn.  K_j and
+        // V_j follow each other in the ring; K_{j+1} is one slot past V_j.
+        for (int j = -1; j < x.steps && ok; ++j) {
+          const uint32_t vs = slot, vphase = phase;
+          if (j >= 0) {
+            advance();
+            ok = mbar_wait(&sb.full[vs], vphase, abortp, spin);
+            if (ok && j >= x.fix) {
+              ok = mbar_wait(&sb.fixed[vs], (fixpar >> vs) & 1, abortp, spin);
+              fixpar ^= 1u << vs;
+            }
           }
-        }
-        if (ok && j + 1 < nb) ok = warp_wait(&sb.full[sk], (rk / C::SLOTS) & 1, abortp, spin);
+          const uint32_t ks = slot;
+          if (ok && j + 1 < x.steps) ok = mbar_wait(&sb.full[ks], phase, abortp, spin);
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (ok && j >= 0 && j < x.nb[w]) {
-            if (j == 0 && no[w]) ok = warp_wait(&sb.oempty[w], (no[w] - 1) & 1, abortp, spin);
-            ok = ok && warp_wait(&sb.pfull[w], np[w] & 1, abortp, spin);
-            ++np[w];
-            if (ok) {
-              fence_after();
-              mma_pv64(tO + 128 * w, tS + 128 * w, sw128_desc(vb, BOX, 1024), id_pv, j != 0);
-              mma_pv64(tO + 128 * w, tS + 128 * w + 32, sw128_desc(vb + 8192, BOX, 1024), id_pv, 1);
-              if (j == x.nb[w] - 1) {
-                commit_elected(&sb.ofull[w]);
-                ++no[w];
+          for (int w = 0; w < 2; ++w) {
+            if (ok && j >= 0 && j < x.nb[w]) {
+              if (j == 0 && no[w]) ok = mbar_wait(&sb.oempty[w], (no[w] - 1) & 1, abortp, spin);
+              ok = ok && mbar_wait(&sb.pfull[w], np[w] & 1, abortp, spin);
+              ++np[w];
+              if (ok) {
+                fence_after();
+                mma_pv(tO + 128 * w, tS + 128 * w, dv0 + vs * STEP, id_pv, j != 0);
+                if (j == x.nb[w] - 1) {
+                  mma_commit(&sb.ofull[w]);
+                  ++no[w];
+                }
+              }
+            }
+            if (ok && j + 1 < x.nb[w]) {
+              if (j < 0) {
+                ok = mbar_wait(&sb.qfull[w], nq[w] & 1, abortp, spin);
+                ++nq[w];
+              }
+              if (ok) {
+                fence_after();
+                mma_qk<C::BOXES>(tS + 128 * w, dq0 + w * STEP, dk0 + ks * STEP, id_qk);
+                mma_commit(&sb.sfull[w]);
+                if (j + 2 == x.nb[w]) mma_commit(&sb.qempty[w]);
               }
             }
           }
-          if (ok && j + 1 < x.nb[w]) {
-            if (j < 0) ok = warp_wait(&sb.qfull[w], (nq >> (16 * w)) & 1, abortp, spin);
-            if (ok) {
-              fence_after();
-              mma_qk<C::BOXES>(tS + 128 * w, sw128_desc(sq + w * C::TILE, 16, 1024), sw128_desc(kb, 16, 1024), id_qk);
-              commit_elected(&sb.sfull[w]);
-              if (j + 2 == x.nb[w]) commit_elected(&sb.qempty[w]);
-            }
+          if (ok && j >= 0) mma_commit(&sb.empty[vs]);
+          if (ok && j + 1 < x.steps) {
+            mma_commit(&sb.empty[ks]);
+            advance();
           }
         }
-        if (ok && j >= 0) commit_elected(&sb.empty[sv]);
-        if (ok && j + 1 < nb) commit_elected(&sb.empty[sk]);
+        mbar_arrive(&sb.iempty[iq.slot]);
+        iq.step();
       }
-      // q tiles loaded so far, one bit (the phase) per tile
-      if (x.nb[0]) nq ^= 1u;
-      if (x.nb[1]) nq ^= 1u << 16;
-      r += 2 * (uint32_t)nb;
-      if (!ok && lane == 0) *abortp = 1;
+      if (!ok) *abortp = 1;
+      mma_commit(&sb.drain);     // every MMA issued has finished before tensor memory is released
+      mbar_wait(&sb.drain, 0, kDrainLimit);
     }
-    commit_elected(&sb.drain);     // every MMA issued has finished before tensor memory is released
-    mbar_wait(&sb.drain, 0, kDrainLimit);
     __syncwarp();
   } else if (warp < 4) {
     // ---------------------------------------------------------------- unseen values of V
-    uint32_t r = 0;
+    Ring<C::SLOTS> rg;
+    Ring<kQueue> iq;
     int item = 0;
     bool ok = true;
     const int tid = threadIdx.x - 64;
-    while (ok && next_item(a, it, x, bad)) {
-      const int nb = max(x.nb[0], x.nb[1]);
+    while (ok) {
+      ok = warp_wait(&sb.ifull[iq.slot], iq.phase, abortp, spin);
+      if (!ok) break;
+      const Item x = sb.item[iq.slot];
+      if (x.len < 0) break;
       // The fixers pass every slot in order, also those they leave alone: a slot's barrier is
       // waited on by parity, which tells neighbouring phases apart and no more.
-      for (int j2 = 0; j2 < 2 * nb; ++j2) {
-        const uint32_t rv = r + (uint32_t)j2;
-        const int s = (int)(rv % C::SLOTS), j = j2 >> 1;
-        ok = mbar_wait(&sb.full[s], (rv / C::SLOTS) & 1, abortp, spin);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
-          if (lane == 0) *abortp = 1;
-          break;
-        }
+      for (int j2 = 0; j2 < 2 * x.steps; ++j2, rg.step()) {
+        const int j = j2 >> 1;
+        ok = warp_wait(&sb.full[rg.slot], rg.phase, abortp, spin);
+        if (!ok) break;
         if (!(j2 & 1) || j < x.fix) {
-          if (lane == 0) mbar_arrive(&sb.empty[s]);
+          if (lane == 0) mbar_arrive(&sb.empty[rg.slot]);
           continue;
         }
         const int live = x.len - j * KEYS;        // rows of this block inside the sequence
-        uint4* tile = reinterpret_cast<uint4*>(ring + s * C::TILE);
+        uint4* tile = reinterpret_cast<uint4*>(ring + rg.slot * C::TILE);
         bool found = false;
-        for (int i = tid; i < C::TILE / 16; i += 64) {
-          const int row = (i >> 3) & 127;
-          if (row >= live) {
-            tile[i] = make_uint4(0, 0, 0, 0);
-          } else if (a.causal) {
-            uint4 u = tile[i];
-            uint32_t wd[4] = {u.x, u.y, u.z, u.w};
-            bool hit = false;
+        for (int i0 = tid; i0 < C::TILE / 16; i0 += 64 * 8) {
+          uint4 u[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if ((wd[q] & 0x7f80u) == 0x7f80u) {
-                wd[q] &= 0xffff0000u;
-                hit = true;
+          for (int q = 0; q < 8; ++q) u[q] = tile[i0 + 64 * q];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            uint32_t wd[4] = {u[q].x, u[q].y, u[q].z, u[q].w};
+            if ((((i0 + 64 * q) >> 3) & 127) >= live) {
+              tile[i0 + 64 * q] = make_uint4(0, 0, 0, 0);
+            } else if (a.causal) {
+              bool hit = false;
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                hit = hit || (wd[z] & 0x7f80u) == 0x7f80u || (wd[z] & 0x7f800000u) == 0x7f800000u;
+              if (hit) {
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                  if ((wd[z] & 0x7f80u) == 0x7f80u) wd[z] &= 0xffff0000u;
+                  if ((wd[z] & 0x7f800000u) == 0x7f800000u) wd[z] &= 0x0000ffffu;
+                }
+                tile[i0 + 64 * q] = make_uint4(wd[0], wd[1], wd[2], wd[3]);
+                found = true;
               }
-              if ((wd[q] & 0x7f800000u) == 0x7f800000u) {
-                wd[q] &= 0x0000ffffu;
-                hit = true;
-              }
-            }
-            if (hit) {
-              tile[i] = make_uint4(wd[0], wd[1], wd[2], wd[3]);
-              found = true;
             }
           }
         }
-        if (found) *(volatile int*)&sb.vbad[item & (kFlags - 1)] = item + 1;
+        if (found) *(volatile int*)&sb.vbad[iq.slot] = item + 1;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&sb.fixed[s]);
-          mbar_arrive(&sb.empty[s]);
+          mbar_arrive(&sb.fixed[rg.slot]);
+          mbar_arrive(&sb.empty[rg.slot]);
         }
       }
-      r += 2 * (uint32_t)nb;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sb.iempty[iq.slot]);
+      iq.step();
       ++item;
     }
+    if (!ok && lane == 0) *abortp = 1;
   }
   } else {
     // ---------------------------------------------------------------- softmax and output
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int w = (warp - 4) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const int tok_in = row / a.group, head_in = row - tok_in * a.group;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t myS = tS + 128 * w + lanes, myO = tO + 128 * w + lanes;
-    uint32_t ns = 0, no = 0;
+    Ring<kQueue> iq;
+    uint32_t ns = 0, no = 0;         // blocks and outputs so far
     int item = 0;
     bool ok = true;
-    while (next_item(a, it, x, bad)) {
-      const int nb = x.nb[w];
-      const int tok = x.tok[w] + tok_in;
-      const int seen = a.causal ? min(x.len, tok + 1) : x.len;     // keys this row sees
-      const int whole = a.causal ? min(x.len, x.tok[w] + 1) : x.len;   // keys every row of the tile sees
-      const bool mine = tok_in < a.tq && tok < x.len;              // a row of the output
+    while (true) {
+      ok = warp_wait(&sb.ifull[iq.slot], iq.phase, abortp, spin);
+      if (!ok) break;
+      const Item& xi = sb.item[iq.slot];
+      const int begin = xi.begin, len = xi.len, hk = xi.hk, tok0 = xi.tok + w * a.tq, nb = xi.nb[w], fix = xi.fix;
+      if (len < 0) break;
+      const int tok = tok0 + tok_in;
+      const int seen = a.causal ? min(len, tok + 1) : len;         // keys this row sees
+      const int whole = a.causal ? min(len, tok0 + 1) : len;       // keys every row of the tile sees
+      const bool mine = tok_in < a.tq && tok < len;                // a row of the output
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < nb; ++j) {
-        if (ok) {
-          ok = mbar_wait(&sb.sfull[w], ns & 1, abortp, spin);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok && lane == 0) {
-            *abortp = 1;
-            if (a.st) set_error(a.st, PWP_ETIMEOUT, kSiteAttention);
-          }
-        }
+        ok = warp_wait(&sb.sfull[w], ns & 1, abortp, spin);
         if (!ok) break;
         ++ns;
         fence_after();
@@ -601,58 +626,79 @@ __global__ void __launch_bounds__(kThreadsAtt, 1)
         const float2 l2 = unpair(add2(sum2[0], sum2[1]));
         l += l2.x + l2.y;
       }
+      if (!ok) break;
       if (nb > 0) {
-        if (ok) {
-          ok = mbar_wait(&sb.ofull[w], no & 1, abortp, spin);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok && lane == 0) {
-            *abortp = 1;
-            if (a.st) set_error(a.st, PWP_ETIMEOUT, kSiteAttention);
-          }
-        }
+        ok = warp_wait(&sb.ofull[w], no & 1, abortp, spin);
+        if (!ok) break;
         ++no;
         fence_after();
         const float inv = 1.f / l;
-        bf16* out = a.out + (long long)(x.begin + tok) * a.os0 + (long long)(x.hk * a.group + head_in) * a.os1;
-        const bool vbad = *(volatile int*)&sb.vbad[item & (kFlags - 1)] == item + 1;
+        bf16* out = a.out + (long long)(begin + tok) * a.os0 + (long long)(hk * a.group + head_in) * a.os1;
+        const bool vbad = *(volatile int*)&sb.vbad[iq.slot] == item + 1;
 #pragma unroll 1
-        for (int ch = 0; ch < D; ch += 16) {
-          float o[16];
-          tmem_ld16(myO + ch, o);
-          if (ch + 16 >= D) {        // the last read of O
+        for (int ch = 0; ch < D; ch += 64) {
+          float o[64];
+          tmem_ld32_nowait(myO + ch, o);
+          tmem_ld32_nowait(myO + ch + 32, o + 32);
+          tmem_wait_ld();
+          pin32(o);
+          pin32(o + 32);
+          if (ch + 64 >= D) {        // the last read of O
             fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sb.oempty[w]);
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = ok ? o[i] * inv : __int_as_float(0x7fc00000);
+          for (int i = 0; i < 64; ++i) o[i] *= inv;
           if (mine && ch < a.d) {
             if (vbad) {
-              for (int key = x.fix * KEYS; key < seen; ++key) {
-                const bf16* vp = a.v + (long long)(x.begin + key) * a.vs0 + (long long)x.hk * a.vs1 + ch;
+              for (int key = fix * KEYS; key < seen; ++key) {
+                const bf16* vp = a.v + (long long)(begin + key) * a.vs0 + (long long)hk * a.vs1 + ch;
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
+                for (int i = 0; i < 64; ++i)
                   if (ch + i < a.d) {
                     const float vv = to_f32(vp[i]);
                     if (!(fabsf(vv) < INFINITY)) o[i] += vv;
                   }
               }
             }
-            if (a.vec && ch + 16 <= a.d) {
-              *reinterpret_cast<uint4*>(out + ch) =
-                  make_uint4(pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
-              *reinterpret_cast<uint4*>(out + ch + 8) =
-                  make_uint4(pack2(o[8], o[9]), pack2(o[10], o[11]), pack2(o[12], o[13]), pack2(o[14], o[15]));
-            } else {
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (ch + i < a.d) out[ch + i] = from_f32<bf16>(o[i]);
+            for (int q = 0; q < 8; ++q) {
+              if (a.vec) {       // d is a multiple of 8
+                if (ch + 8 * q < a.d)
+                  *reinterpret_cast<uint4*>(out + ch + 8 * q) =
+                      make_uint4(pack2(o[8 * q], o[8 * q + 1]), pack2(o[8 * q + 2], o[8 * q + 3]),
+                                 pack2(o[8 * q + 4], o[8 * q + 5]), pack2(o[8 * q + 6], o[8 * q + 7]));
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (ch + 8 * q + i < a.d) out[ch + 8 * q + i] = from_f32<bf16>(o[8 * q + i]);
+              }
             }
           }
           __syncwarp();
         }
       }
+      if (lane == 0) mbar_arrive(&sb.iempty[iq.slot]);
+      iq.step();
       ++item;
+    }
+    if (!ok) {
+      // gave up: this item's rows and all later ones come out NaN
+      if (lane == 0) {
+        *abortp = 1;
+        if (a.st) set_error(a.st, PWP_ETIMEOUT, kSiteAttention);
+      }
+      __syncwarp();
+      Items it{(int)blockIdx.x, 0, 0};
+      Item x;
+      bool bad = false;
+      for (int i = 0; next_item(a, it, x, bad); ++i) {
+        const int tok = x.tok + w * a.tq + tok_in;
+        if (i < item || tok_in >= a.tq || tok >= x.len) continue;
+        bf16* out = a.out + (long long)(x.begin + tok) * a.os0 + (long long)(x.hk * a.group + head_in) * a.os1;
+        for (int c = 0; c < a.d; ++c) out[c] = from_f32<bf16>(__int_as_float(0x7fc00000));
+      }
     }
   }
 
