@@ -294,7 +294,8 @@ pwp_status pwp_pack_24(const float* W_hat_dev, const uint8_t* mask_dev, int32_t 
  * output can be passed as they are; no alignment beyond the element's own is needed (16-byte
  * aligned bases and strides take the fast kernels).  type is PWP_BF16 or PWP_FP32, the same
  * for every tensor of a call; sums are fp32 and each output is rounded once to its type.
- * A call with no rows enqueues nothing.  No workspace.  stats_dev (linear, attention) is
+ * A call with no rows enqueues nothing.  No workspace,
+ * but for misaligned operands of pwp_linear.  stats_dev (linear, attention) is
  * optional: it receives device-side errors and is not cleared by the call; without it a
  * wait that runs out leaves NaN in the rows it was to write. */
 
@@ -380,8 +381,14 @@ typedef struct {
     pwp_stats* stats_dev;        /* or NULL */
     int64_t rows;
     int32_t k, n, type, activation;
+    void* ws_dev;                /* or NULL */
+    size_t ws_bytes;
 } pwp_linear_args;
 pwp_status pwp_linear(const pwp_linear_args* args, void* stream);
+/* Bytes of scratch (256-byte aligned) that let bf16 operands whose bases or row strides are not
+ * 16-byte aligned take the tensor cores: the call copies them there first.  0 when nothing
+ * is gained by it; without the scratch such a call runs on the CUDA cores. */
+size_t pwp_linear_workspace_bytes(const pwp_linear_args* args);
 
 /* Prune without a caller-provided workspace (the pages have no counterpart: this is a
  * convenience of this library).  For callers that cannot allocate device memory when

@@ -36,13 +36,14 @@ FEEDS = {"q_proj": "attn_in", "k_proj": "attn_in", "v_proj": "attn_in", "o_proj"
 # small operator's time is mostly its host side
 ROPE_ARGS = struct.Struct("@4P8q4Pq6i2f")
 ATTENTION_ARGS = struct.Struct("@4P8q2Pq6if4x")
-LINEAR_ARGS = struct.Struct("@7P5qPq4i")
+LINEAR_ARGS = struct.Struct("@7P5qPq4iPN")
 
 SIGNATURES = {
     "pwp_rms_norm": (_i32, [_vp, _i32, _i64, _i32, _i64, _vp, _f32, _vp, _i64, _vp]),
     "pwp_qk_norm_rope": (_i32, [ctypes.c_char_p, _vp]),
     "pwp_attention": (_i32, [ctypes.c_char_p, _vp]),
     "pwp_linear": (_i32, [ctypes.c_char_p, _vp]),
+    "pwp_linear_workspace_bytes": (ctypes.c_size_t, [ctypes.c_char_p]),
 }
 
 
@@ -352,11 +353,21 @@ def _linear(x, w, w_up, bias, bias_up, activation, residual, out, stats, name):
     else:
         _check_out(out, "out", (rows, n), x)
     if rows:
-        _call("pwp_linear", LINEAR_ARGS.pack(
-            x.data_ptr(), w.data_ptr(), _ptr(w_up), _ptr(bias), _ptr(bias_up), _ptr(residual), out.data_ptr(),
-            x.stride(0), w.stride(0), w_up.stride(0) if w_up is not None else 0,
-            residual.stride(0) if residual is not None else 0, out.stride(0), stats_p, rows, k, n, code, act),
-            x.get_device())
+        xs, ws = x.stride(0), w.stride(0)
+        us = w_up.stride(0) if w_up is not None else 0
+        xp, wp, up = x.data_ptr(), w.data_ptr(), _ptr(w_up)
+        args = (xp, wp, up, _ptr(bias), _ptr(bias_up), _ptr(residual), out.data_ptr(), xs, ws, us,
+                residual.stride(0) if residual is not None else 0, out.stride(0), stats_p, rows, k, n, code, act)
+        scratch = None
+        if code == _pwp.BF16 and ((xs | ws | us) & 7 or (xp | wp | up) & 15):
+            # operands the tensor cores' copies cannot take as they are
+            need = _pwp.lib().pwp_linear_workspace_bytes(LINEAR_ARGS.pack(*args, 0, 0))
+            if need:
+                scratch = _pwp._torch().empty(need, dtype=_pwp._torch().uint8, device=x.device)
+                args += (scratch.data_ptr(), need)
+        if scratch is None:
+            args += (0, 0)
+        _call("pwp_linear", LINEAR_ARGS.pack(*args), x.get_device())
     return out
 
 

@@ -52,17 +52,31 @@ pwp_status pwp_attention(const pwp_attention_args* a, void* stream) {
   return status_of(used || e != cudaSuccess ? e : launch_attention_simt(*a, (cudaStream_t)stream));
 }
 
-pwp_status pwp_linear(const pwp_linear_args* a, void* stream) {
+static bool valid_linear(const pwp_linear_args* a) {
   if (!a || !valid_type(a->type) || a->rows < 0 || a->rows > 0x7fffffffLL || a->k < 1 || a->n < 1 ||
       a->k >= (1 << 24) || a->n >= (1 << 24) || a->activation < PWP_ACT_NONE || a->activation > PWP_ACT_GELU_TANH ||
       a->x_stride < 0 || a->w_stride < 0 || a->w_up_stride < 0 || a->residual_stride < 0 || a->out_stride < 0 ||
       (!a->w_up_dev && a->bias_up_dev))
-    return PWP_EINVAL;
+    return false;
+  return a->rows == 0 || (a->x_dev && a->w_dev && a->out_dev && (a->rows == 1 || a->out_stride >= a->n));
+}
+
+size_t pwp_linear_workspace_bytes(const pwp_linear_args* a) {
+  return valid_linear(a) && a->rows > 0 ? linear_align_bytes(*a) : 0;
+}
+
+pwp_status pwp_linear(const pwp_linear_args* a, void* stream) {
+  if (!valid_linear(a)) return PWP_EINVAL;
   if (a->rows == 0) return PWP_OK;
-  if (!a->x_dev || !a->w_dev || !a->out_dev || (a->rows > 1 && a->out_stride < a->n)) return PWP_EINVAL;
+  if (a->ws_dev && ((uintptr_t)a->ws_dev & 255) != 0) return PWP_EWORKSPACE;
+  cudaStream_t s = (cudaStream_t)stream;
+  pwp_linear_args b = *a;
+  cudaError_t e = cudaSuccess;
+  const size_t need = linear_align_bytes(*a);
+  if (need && a->ws_dev && a->ws_bytes >= need) e = launch_linear_align(b, s);
   bool used = false;
-  const cudaError_t e = launch_linear_tc(*a, (cudaStream_t)stream, &used);
-  return status_of(used || e != cudaSuccess ? e : launch_linear_simt(*a, (cudaStream_t)stream));
+  if (e == cudaSuccess) e = launch_linear_tc(b, s, &used);
+  return status_of(used || e != cudaSuccess ? e : launch_linear_simt(*a, s));
 }
 
 }  // extern "C"

@@ -26,12 +26,56 @@ __device__ __forceinline__ float activate(int act, float x) {
     case PWP_ACT_RELU: return x != x ? x : fmaxf(x, 0.f);
     case PWP_ACT_SILU: return __fdividef(x, 1.f + __expf(-x));
     case PWP_ACT_GELU: return 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
-    case PWP_ACT_GELU_TANH: {
-      const float t = 0.79788456080286536f * (x + 0.044715f * x * x * x);
-      return 0.5f * x * (1.f + tanhf(t));
-    }
+    case PWP_ACT_GELU_TANH:      // (1 + tanh t) / 2 = 1 / (1 + e^-2t)
+      return __fdividef(x, 1.f + __expf(-1.5957691216057308f * (x + 0.044715f * x * x * x)));
     default: return x;
   }
+}
+
+// Two fp32 operations in one instruction.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// Thread-block clusters: this CTA's rank, a barrier of all its threads, and stores into another
+// CTA's shared memory.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the address, in the cluster's window, of a shared-memory address of this CTA as CTA `rank` has it
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void remote_store4(uint32_t addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void remote_store(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // One tile of a packed batch: rows [begin + first, begin + first + per) of the sequence
@@ -85,6 +129,8 @@ cudaError_t launch_qk_norm_rope(const pwp_rope_args& a, cudaStream_t s);
 cudaError_t launch_attention_simt(const pwp_attention_args& a, cudaStream_t s);
 cudaError_t launch_attention_tc(const pwp_attention_args& a, cudaStream_t s, bool* used);
 cudaError_t launch_linear_simt(const pwp_linear_args& a, cudaStream_t s);
+size_t linear_align_bytes(const pwp_linear_args& a);
+cudaError_t launch_linear_align(pwp_linear_args& a, cudaStream_t s);
 cudaError_t launch_linear_tc(const pwp_linear_args& a, cudaStream_t s, bool* used);
 
 }  // namespace pwp

@@ -34,26 +34,8 @@ typedef __nv_bfloat16 bf16;
 constexpr int TK = 64;                            // k per stage: one 128-byte swizzled row
 constexpr int ROW_BYTES = TK * 2;
 
-// ---------------------------------------------------------------- cluster helpers
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// the address, in the cluster's window, of a shared-memory address of this CTA as CTA `rank` has it
-__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
 __device__ __forceinline__ void remote_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void remote_store(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 // A tile load of a CTA pair: into this CTA's shared memory, counted by the barrier at `bar`
 // (a cluster address: the leader's).
@@ -791,6 +773,67 @@ cudaError_t run_skinny(const pwp_linear_args& a, const Epilogue& ep, cudaStream_
 }
 
 }  // namespace
+
+// ---------------------------------------------------------------- operands that are not 16-byte aligned
+
+namespace {
+
+// rows of k values from a stride of `stride` to one of `kp` (a multiple of 8); one 16-byte piece per
+// thread and step.  What lies between k and kp is never read as data.
+__global__ void __launch_bounds__(256) align_rows_kernel(const bf16* __restrict__ src, long long stride, long long rows,
+                                                         int k, int kp, bf16* __restrict__ dst) {
+  const int pieces = kp / 8;
+  const long long total = rows * pieces;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += 256LL * gridDim.x) {
+    const long long r = i / pieces;
+    const int c = (int)(i - r * pieces) * 8;
+    const bf16* p = src + r * stride + c;
+    uint16_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < k ? *reinterpret_cast<const uint16_t*>(p + j) : (uint16_t)0;
+    *reinterpret_cast<uint4*>(dst + r * kp + c) =
+        make_uint4(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16, v[4] | (uint32_t)v[5] << 16,
+                   v[6] | (uint32_t)v[7] << 16);
+  }
+}
+
+bool misaligned(const void* p, long long stride, long long rows) {
+  return p && (((uintptr_t)p & 15) != 0 || (rows > 1 && (stride & 7) != 0));
+}
+size_t copy_bytes(long long rows, int k) { return ((size_t)rows * ((k + 7) & ~7) * 2 + 255) & ~(size_t)255; }
+
+}  // namespace
+
+// Copying costs one more read and write of an operand; below 2^24 multiplications the CUDA
+// cores are done as soon.
+size_t linear_align_bytes(const pwp_linear_args& a) {
+  if (a.type != PWP_BF16 || (double)a.rows * a.k * a.n < (double)(1 << 24)) return 0;
+  size_t n = 0;
+  if (misaligned(a.x_dev, a.x_stride, a.rows)) n += copy_bytes(a.rows, a.k);
+  if (misaligned(a.w_dev, a.w_stride, a.n)) n += copy_bytes(a.n, a.k);
+  if (misaligned(a.w_up_dev, a.w_up_stride, a.n)) n += copy_bytes(a.n, a.k);
+  return n;
+}
+
+// Copies the misaligned operands into a.ws_dev and points `a` at the copies.
+cudaError_t launch_linear_align(pwp_linear_args& a, cudaStream_t s) {
+  char* ws = (char*)a.ws_dev;
+  const int kp = (a.k + 7) & ~7;
+  auto copy = [&](const void*& p, int64_t& stride, long long rows) {
+    if (!misaligned(p, stride, rows)) return;
+    const long long blocks = (rows * (kp / 8) + 255) / 256;
+    align_rows_kernel<<<(unsigned)(blocks < 16 * kNumSM ? blocks : 16 * kNumSM), 256, 0, s>>>((const bf16*)p, stride, rows,
+                                                                                            a.k, kp, (bf16*)ws);
+    count_launches(1);
+    p = ws;
+    stride = kp;
+    ws += copy_bytes(rows, a.k);
+  };
+  copy(a.x_dev, a.x_stride, a.rows);
+  copy(a.w_dev, a.w_stride, a.n);
+  copy(a.w_up_dev, a.w_up_stride, a.n);
+  return cudaGetLastError();
+}
 
 // Declines (used = false) when the tensors do not meet the copies' rules (16-byte aligned
 // bases, row strides a multiple of 16 bytes).

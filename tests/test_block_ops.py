@@ -116,10 +116,11 @@ class LinearArgs(ctypes.Structure):
     _fields_ = [("x", _vp), ("w", _vp), ("w_up", _vp), ("bias", _vp), ("bias_up", _vp), ("residual", _vp),
                 ("out", _vp), ("x_stride", _i64), ("w_stride", _i64), ("w_up_stride", _i64),
                 ("residual_stride", _i64), ("out_stride", _i64), ("stats", _vp), ("rows", _i64), ("k", _i32),
-                ("n", _i32), ("type", _i32), ("activation", _i32)]
+                ("n", _i32), ("type", _i32), ("activation", _i32), ("ws", _vp), ("ws_bytes", ctypes.c_size_t)]
 
 
-ARGS = {"pwp_qk_norm_rope": RopeArgs, "pwp_attention": AttentionArgs, "pwp_linear": LinearArgs}
+ARGS = {"pwp_qk_norm_rope": RopeArgs, "pwp_attention": AttentionArgs, "pwp_linear": LinearArgs,
+        "pwp_linear_workspace_bytes": LinearArgs}
 
 
 class _FakeLib:
@@ -217,7 +218,7 @@ def test_refusals(fake, call, err):
 def test_no_grad_lets_parameters_through(fake):
     with torch.no_grad():
         pwp.linear(z(2, 4), z(3, 4).requires_grad_())
-    assert len(fake.calls) == 1
+    assert [name for name, _ in fake.calls].count("pwp_linear") == 1
 
 
 def test_calls_without_rows_launch_nothing(fake):
@@ -262,6 +263,36 @@ def test_marshalling(fake):
     assert fake.calls[-1][0] == "pwp_rms_norm" and fake.calls[-1][1][6] == 0.5
 
 
+def test_misaligned_operands_get_scratch(fake, monkeypatch):
+    sizes = []
+    monkeypatch.setattr(_FakeLib, "pwp_linear_workspace_bytes", lambda self, a: sizes.append(a) or 512, raising=False)
+    x = z(3, 24)[:, 1:17]
+    pwp.linear(x, z(8, 16))
+    a = fake.calls[-1][1][0]
+    assert len(sizes) == 1 and a.ws and a.ws_bytes == 512
+    pwp.linear(z(3, 16), z(8, 16))
+    a = fake.calls[-1][1][0]
+    assert a.x % 16 or (len(sizes) == 1 and a.ws is None and a.ws_bytes == 0)
+
+
+def test_workspace_bytes_of_misaligned_operands():
+    L = pwp.lib()
+
+    def need(**kw):
+        a = LinearArgs(x=256, w=256, out=256, rows=300, k=1001, n=400, x_stride=1008, w_stride=1008, out_stride=400)
+        for key, val in kw.items():
+            setattr(a, key, val)
+        return L.pwp_linear_workspace_bytes(bytes(a))
+    assert need() == 0
+    assert need(x_stride=1001) == (300 * 1008 * 2 + 255) // 256 * 256
+    assert need(w=258) == (400 * 1008 * 2 + 255) // 256 * 256
+    assert need(w_stride=1001, w_up=256, w_up_stride=1001) == 2 * ((400 * 1008 * 2 + 255) // 256 * 256)
+    assert need(x_stride=1001, rows=1) == 0                 # too little work, and one row has no stride
+    assert need(x_stride=1001, type=1) == 0 and need(k=0) == 0
+    a = LinearArgs(x=256, w=256, out=256, rows=2, k=4, n=4, x_stride=4, w_stride=4, out_stride=4, ws=264, ws_bytes=99)
+    assert L.pwp_linear(bytes(a), None) == 3
+
+
 def test_block_forward_refusals(fake):
     w = {p: z(8, 8) for p in B.FEEDS}
     with pytest.raises(ValueError, match="missing"):
@@ -293,7 +324,7 @@ def test_struct_sizes_match_the_header(tmp_path):
                    check=True)
     got = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()
     assert [int(x) for x in got] == [s.size for s in (B.ROPE_ARGS, B.ATTENTION_ARGS, B.LINEAR_ARGS)]
-    assert [int(x) for x in got] == [ctypes.sizeof(t) for t in ARGS.values()]
+    assert [int(x) for x in got] == [ctypes.sizeof(t) for t in (RopeArgs, AttentionArgs, LinearArgs)]
 
 
 def test_c_entry_points_check_their_arguments():

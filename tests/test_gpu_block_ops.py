@@ -302,7 +302,9 @@ ACTS = ["none", "relu", "silu", "gelu", "gelu_tanh"]
     (1, 1, 1, "bf16"), (1, 64, 128, "bf16"), (1, 4096, 520, "bf16"), (3, 200, 24, "bf16"), (17, 1000, 136, "bf16"),
     (64, 256, 256, "bf16"), (129, 72, 1000, "bf16"), (300, 520, 264, "bf16"), (256, 128, 512, "bf16"),
     (700, 640, 1032, "bf16"), (33, 100, 77, "bf16"), (5, 33, 40, "bf16"), (260, 8, 8, "bf16"), (1100, 512, 1536, "bf16"),
-    (1, 5, 3, "fp32"), (70, 130, 65, "fp32"), (200, 64, 128, "fp32"),
+    (700, 333, 521, "bf16"), (1400, 401, 1043, "bf16"), (40, 1003, 1001, "bf16"),
+    (1, 5, 3, "fp32"), (70, 130, 65, "fp32"), (200, 64, 128, "fp32"), (300, 515, 260, "fp32"), (130, 4100, 132, "fp32"),
+    (33, 2000, 36, "fp32"), (1, 700, 200, "fp32"), (1100, 36, 900, "fp32"),
 ])
 def test_linear_and_gated(rows, k, n, dtype):
     pwp = _pwp()
