@@ -47,6 +47,18 @@ SIGNATURES = {
 }
 
 
+_loaded = None
+
+
+def _torch():
+    """torch, imported at the first call (looking it up again costs a small operator's call
+    as much as its launch checks)."""
+    global _loaded
+    if _loaded is None:
+        _loaded = _pwp._torch()
+    return _loaded
+
+
 # ------------------------------------------------------------------- argument checks
 
 def _operator(fn):
@@ -62,11 +74,11 @@ def _operator(fn):
             dev = x.get_device()
         except AttributeError:
             raise TypeError(f"{fn.__name__}: {first}: tensor expected, got {type(x).__name__}") from None
-        call = fn if kw.get("stream") is None else on_stream
-        torch = _pwp._torch()
-        if dev < 0 or dev == torch.cuda.current_device():
+        call = on_stream if "stream" in kw and kw["stream"] is not None else fn
+        cuda = _torch().cuda
+        if dev < 0 or dev == cuda.current_device():
             return call(*a, **kw)
-        with torch.cuda.device(dev):
+        with cuda.device(dev):
             return call(*a, **kw)
     return wrapped
 
@@ -76,12 +88,12 @@ def _on_gpu(t):
 
 
 def _stream_of(dev):
-    return _pwp._torch()._C._cuda_getCurrentRawStream(dev)
+    return _torch()._C._cuda_getCurrentRawStream(dev)
 
 
 def _type_code(x, name, dims):
     """PWP_BF16 or PWP_FP32 of an operator's first tensor, whose form is checked."""
-    torch = _pwp._torch()
+    torch = _torch()
     code = _pwp.BF16 if x.dtype is torch.bfloat16 else _pwp.FP32 if x.dtype is torch.float32 else None
     if code is None:
         _pwp._dtype_code(x)       # raises
@@ -122,7 +134,7 @@ def _check_out(t, name, shape, like):
 
 
 def _forward_only(*ts):
-    if _pwp._torch().is_grad_enabled():
+    if _torch().is_grad_enabled():
         for t in ts:
             if t is not None and t.requires_grad:
                 raise ValueError("the operators compute a forward pass only: call them under torch.no_grad() "
@@ -136,7 +148,7 @@ def _ptr(t):
 def _stats_ptr(stats, like):
     if stats is None:
         return 0
-    _check_tensor(stats, "stats", (ctypes.sizeof(_pwp.Stats),), like, _pwp._torch().uint8)
+    _check_tensor(stats, "stats", (ctypes.sizeof(_pwp.Stats),), like, _torch().uint8)
     return stats.data_ptr()
 
 
@@ -158,7 +170,7 @@ def rms_norm(x, weight=None, *, eps=1e-5, out=None, stream=None):
         raise ValueError(f"x: width {width}, 1 to 65536 expected")
     if weight is not None:
         _check_tensor(weight, "weight", (width,), x)
-    if not (eps >= 0 and math.isfinite(eps)):
+    if not 0 <= eps < math.inf:
         raise ValueError(f"eps: {eps}")
     _forward_only(x, weight)
     if out is None:
@@ -189,7 +201,7 @@ def rope_frequencies(rot, *, base=10000.0, scaling=None, device="cuda"):
        "beta_slow": 1.0}                     the same idea with the ramp linear in the pair's
                                              index, between the pairs that make beta_fast and
                                              beta_slow turns; factor 0.1 ln s + 1"""
-    torch = _pwp._torch()
+    torch = _torch()
     rot = int(rot)
     if rot < 0 or rot % 2 or not base > 0:
         raise ValueError(f"rot even and base > 0 expected, got {rot} and {base}")
@@ -240,7 +252,7 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     q_weight, k_weight: [d], the head norms' weights, or None for no norm.  layout "half" pairs
     elements i and i + rot/2, "interleaved" 2i and 2i+1.  q_out / k_out: None, tensors of the
     same shapes, or q / k themselves.  Returns (q_out, k_out)."""
-    torch = _pwp._torch()
+    torch = _torch()
     code = _type_code(q, "q", 3)
     n, hq, d = q_shape = q.shape
     if k.dim() != 3:
@@ -257,7 +269,7 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
         raise ValueError(f"head size {d} (1 to 1024), {rot} elements turned")
     if layout not in LAYOUTS:
         raise ValueError(f"layout: {layout!r}, one of {sorted(LAYOUTS)} expected")
-    if not (eps >= 0 and math.isfinite(eps) and math.isfinite(factor)):
+    if not (0 <= eps < math.inf and math.isfinite(factor)):
         raise ValueError(f"eps {eps}, factor {factor}")
     if q_weight is not None:
         _check_tensor(q_weight, "q_weight", (d,), q)
@@ -306,7 +318,7 @@ def attention(q, k, v, cu_seqlens, *, causal=True, scale=None, out=None, stats=N
         raise ValueError(f"{n} tokens of {hq} heads: fewer than 2^31 query rows expected")
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError(f"cu_seqlens: [sequences + 1] expected, got shape {tuple(cu_seqlens.shape)}")
-    _check_tensor(cu_seqlens, "cu_seqlens", cu_seqlens.shape, q, _pwp._torch().int32)
+    _check_tensor(cu_seqlens, "cu_seqlens", cu_seqlens.shape, q, _torch().int32)
     if scale is None:
         scale = d ** -0.5
     elif not math.isfinite(scale):
@@ -363,7 +375,7 @@ def _linear(x, w, w_up, bias, bias_up, activation, residual, out, stats, name):
             # operands the tensor cores' copies cannot take as they are
             need = _pwp.lib().pwp_linear_workspace_bytes(LINEAR_ARGS.pack(*args, 0, 0))
             if need:
-                scratch = _pwp._torch().empty(need, dtype=_pwp._torch().uint8, device=x.device)
+                scratch = _torch().empty(need, dtype=_torch().uint8, device=x.device)
                 args += (scratch.data_ptr(), need)
         if scratch is None:
             args += (0, 0)
@@ -409,7 +421,7 @@ def block_forward(weights, hidden, seq_lens, *, heads, kv_heads=None, freqs=None
     Returns (activations, out): {"attn_in", "o_in", "mlp_in", "down_in"}, the inputs of
     the projections as ``FEEDS`` names them (``prune_block``'s activations), and the block's
     output, residuals included.  stats: an optional ``new_stats`` record."""
-    torch = _pwp._torch()
+    torch = _torch()
     missing = sorted(set(FEEDS) - set(weights))
     if missing:
         raise ValueError(f"weights: {missing} missing")
