@@ -31,7 +31,8 @@
 // the time.  The single-thread roles are bound by instruction issue and fetch, so they hold
 // little code: running slots and descriptors and no item search were worth 0.09 ms of 0.70.
 // Tried and slower (full attention): P handed over in halves (1.24 ms, and 1.15 with an MMA warp
-// per tile); blocks of 64 keys with two S per tile (1.42); 32 keys at a time (1.31); the sum in
+// per tile); blocks of 64 keys with two S per tile (1.42); 32 keys at a time (1.31); two threads
+// to a row, 16 softmax warps of 104 registers (1.09); the sum in
 // place of the maximum as the reference's guard (0.99); none (0.97) or three of eight pairs of
 // exponentials (1.19) on the FMA pipe.
 //

@@ -16,7 +16,8 @@
 // over the CTAs of a cluster so that every SM streams weights.  Each CTA then stores its
 // partial sums straight from tensor memory into the shared memory of the CTA that finishes
 // those rows (stores do not wait for the other side, loads from it would), which adds them
-// in rank order -- no atomics, no workspace.  A row of 4096 x 4096 weights: MEASURED_SKINNY.
+// in rank order -- no atomics, no workspace.  One row of 4096 x 4096 bf16 weights:
+// 10.3 us (5.1 at the copy rate), 33 rows of two 11008 x 4096: 34.7 us (27.6).
 //
 // Accumulators are fp32; bias, activation, product and residual are applied in fp32 and the
 // result is rounded to bf16 once.  Every wait is bounded: a wait that runs out records
@@ -160,8 +161,8 @@ __device__ __forceinline__ void activate32(int act, float (&v)[32]) {
 constexpr int P_ROWS = 128;                       // rows of x, and of W, per CTA
 constexpr int P_STAGES = 6;
 constexpr int P_STAGE_BYTES = 2 * P_ROWS * ROW_BYTES;   // 32 KB
-constexpr int P_EPI_WARPS = 8, P_THREADS = 32 * (2 + P_EPI_WARPS);
-constexpr int P_TURN = 32 * 128;                        // a warp's 32 rows of 64 bf16, for its output
+constexpr int P_EPI_WARPS = 16, P_THREADS = 32 * (2 + P_EPI_WARPS);
+constexpr int P_TURN = 32 * 64;                         // a warp's 32 rows of 32 bf16, for its output
 constexpr int P_SMEM = P_STAGES * P_STAGE_BYTES + P_EPI_WARPS * P_TURN + 1024 + 256;
 constexpr int P_ACC_COLS = 256;
 constexpr int P_GROUP = 8;                        // row tiles that share W tiles while they are in L2
@@ -305,7 +306,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
     }
     __syncwarp();
   } else {
-    // warp e reads the tensor-memory lanes 32 (e % 4).. and half of the tile's columns
+    // warp e reads the tensor-memory lanes 32 (e % 4).. and a quarter of the tile's columns
     const int quarter = warp & 3, part = (warp - 2) >> 2;
     int i = 0;
     bool ok = true;
@@ -325,86 +326,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
       const long long rw = (long long)m * 2 * P_ROWS + rank * P_ROWS + quarter * 32, r = rw + lane;   // warp's, thread's row
       const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(a * P_ACC_COLS);
       uint8_t* turn = turn_all + (warp - 2) * P_TURN;
-      // 64 columns at a time.  A thread holds a row, but 32 rows' 16-byte pieces make 32 separate
+      // 32 columns at a time.  A thread holds a row, but 32 rows' 16-byte pieces make 32 separate
       // writes; turned through shared memory (16-byte pieces swizzled by row) a warp writes, and
-      // reads of the residual, four whole 128-byte lines.
-      const int prow = lane >> 3, pcol = lane & 7;
+      // reads of the residual, eight rows' whole 64 bytes.  Sixteen warps, because each spends
+      // most of its time waiting: at 16384 x 128 x 8192, where the epilogue is the bound, plain
+      // 108 us with eight warps of 64 columns and 89 with these, with erf-GELU 300 and 190.
+      const int prow = lane >> 2, pcol = lane & 3;
 #pragma unroll 1
       for (int ch = part * (NT / 128); ch < (part + 1) * (NT / 128); ++ch) {
-        const int c0 = c * NT + ch * 64, avail = n - c0;
+        const int c0 = c * NT + ch * 32, avail = n - c0;
         if (avail <= 0) break;
         const bool on = 8 * pcol < avail;
         if (ep.vec && ep.residual) {
-          uint4 u[8];
+          uint4 w[4];
           const bf16* p = ep.residual + (rw + prow) * ep.residual_stride + c0 + 8 * pcol;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (on && rw + prow + 4 * i < rows) u[i] = *reinterpret_cast<const uint4*>(p + 4 * i * ep.residual_stride);
+          for (int q = 0; q < 4; ++q)
+            if (on && rw + prow + 8 * q < rows) w[q] = *reinterpret_cast<const uint4*>(p + 8 * q * ep.residual_stride);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int q = prow + 4 * i;
-            *reinterpret_cast<uint4*>(turn + q * 128 + ((pcol ^ (q & 7)) << 4)) = u[i];
+          for (int q = 0; q < 4; ++q) {
+            const int z = prow + 8 * q;
+            *reinterpret_cast<uint4*>(turn + z * 64 + ((pcol ^ ((z >> 1) & 3)) << 4)) = w[q];
           }
           __syncwarp();
         }
-        float acc[2][32];
-        tmem_ld32_nowait(base + (uint32_t)(ch * 64), acc[0]);
-        tmem_ld32_nowait(base + (uint32_t)((GATED ? 128 : 32) + ch * 64), acc[1]);
+        float v[32], u[32];
+        tmem_ld32_nowait(base + (uint32_t)(ch * 32), v);
+        if (GATED) tmem_ld32_nowait(base + (uint32_t)(128 + ch * 32), u);
         tmem_wait_ld();
-        pin32(acc[0]);
-        pin32(acc[1]);
+        pin32(v);
+        if (GATED) pin32(u);
+        if (ep.bias) add32(v, ep.bias + c0, avail);
+        activate32(ep.act, v);
+        if (GATED) {
+          if (ep.bias_up) add32(u, ep.bias_up + c0, avail);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int c1 = c0 + 32 * h, left = n - c1;
-          if (left <= 0) break;
-          if (GATED && h == 1) {
-            tmem_ld32_nowait(base + (uint32_t)(32 + ch * 64), acc[0]);
-            tmem_ld32_nowait(base + (uint32_t)(160 + ch * 64), acc[1]);
-            tmem_wait_ld();
-            pin32(acc[0]);
-            pin32(acc[1]);
-          }
-          float(&v)[32] = GATED ? acc[0] : acc[h];
-          float(&u)[32] = acc[1];
-          if (ep.bias) add32(v, ep.bias + c1, left);
-          activate32(ep.act, v);
-          if (GATED) {
-            if (ep.bias_up) add32(u, ep.bias_up + c1, left);
+          for (int j = 0; j < 32; ++j) v[j] *= u[j];
+        }
+        if (!ok) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] *= u[j];
-          }
-          if (!ok) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __int_as_float(0x7fc00000);
-          }
-          if (ep.vec) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint4* at = reinterpret_cast<uint4*>(turn + lane * 128 + (((4 * h + q) ^ (lane & 7)) << 4));
-              if (ep.residual) {
-                float w[8];
-                unpack8(*at, w);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[8 * q + j] += w[j];
-              }
-              *at = make_uint4(pack2(v[8 * q], v[8 * q + 1]), pack2(v[8 * q + 2], v[8 * q + 3]),
-                               pack2(v[8 * q + 4], v[8 * q + 5]), pack2(v[8 * q + 6], v[8 * q + 7]));
-            }
-          } else if (r < rows) {
-            if (ep.residual) add32(v, ep.residual + r * ep.residual_stride + c1, left);
-            store32(ep.out + r * ep.out_stride + c1, v, left);
-          }
+          for (int j = 0; j < 32; ++j) v[j] = __int_as_float(0x7fc00000);
         }
         if (ep.vec) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint4* at = reinterpret_cast<uint4*>(turn + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4));
+            if (ep.residual) {
+              float w[8];
+              unpack8(*at, w);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[8 * q + j] += w[j];
+            }
+            *at = make_uint4(pack2(v[8 * q], v[8 * q + 1]), pack2(v[8 * q + 2], v[8 * q + 3]),
+                             pack2(v[8 * q + 4], v[8 * q + 5]), pack2(v[8 * q + 6], v[8 * q + 7]));
+          }
           __syncwarp();
           bf16* p = ep.out + (rw + prow) * ep.out_stride + c0 + 8 * pcol;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int q = prow + 4 * i;
-            const uint4 u = *reinterpret_cast<const uint4*>(turn + q * 128 + ((pcol ^ (q & 7)) << 4));
-            if (on && rw + q < rows) *reinterpret_cast<uint4*>(p + 4 * i * ep.out_stride) = u;
+          for (int q = 0; q < 4; ++q) {
+            const int z = prow + 8 * q;
+            const uint4 w = *reinterpret_cast<const uint4*>(turn + z * 64 + ((pcol ^ ((z >> 1) & 3)) << 4));
+            if (on && rw + z < rows) *reinterpret_cast<uint4*>(p + 8 * q * ep.out_stride) = w;
           }
           __syncwarp();
+        } else if (r < rows) {
+          if (ep.residual) add32(v, ep.residual + r * ep.residual_stride + c0, avail);
+          store32(ep.out + r * ep.out_stride + c0, v, avail);
         }
       }
       fence_before();
