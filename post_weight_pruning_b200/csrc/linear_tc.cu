@@ -330,7 +330,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
       // writes; turned through shared memory (16-byte pieces swizzled by row) a warp writes, and
       // reads of the residual, eight rows' whole 64 bytes.  Sixteen warps, because each spends
       // most of its time waiting: at 16384 x 128 x 8192, where the epilogue is the bound, plain
-      // 108 us with eight warps of 64 columns and 89 with these, with erf-GELU 300 and 190.
+      // 108 us with eight warps of 64 columns and 89-96 with these, with erf-GELU 300 and 190-199.
       const int prow = lane >> 2, pcol = lane & 3;
 #pragma unroll 1
       for (int ch = part * (NT / 128); ch < (part + 1) * (NT / 128); ++ch) {
