@@ -561,10 +561,13 @@ __global__ void __launch_bounds__(kThreadsAtt, 1)
         if (j == 0) m = max_of(s);
         // The probabilities are formed against the reference of the blocks before, and this
         // block's maximum beside them; only when it has left the reference by more than 8 in
-        // the exponent are o and the sum rescaled and the probabilities formed again.
+        // the exponent are o and the sum rescaled and the probabilities formed again.  A row
+        // moves to a reference that differs from its own, so at most twice (an infinite maximum
+        // stays); a row of -inf alone has the reference 0 and the sum 0, until it sees more.
         f32x2 sum2[2];
         while (true) {
-          const f32x2 c2 = pair(a.c, a.c), mc2 = pair(-m * a.c, -m * a.c);
+          const float mc = m == -INFINITY ? 0.f : -m * a.c;
+          const f32x2 c2 = pair(a.c, a.c), mc2 = pair(mc, mc);
           float mx4[4] = {m, m, m, m};
           sum2[0] = sum2[1] = pair(0.f, 0.f);
 #pragma unroll
@@ -582,7 +585,7 @@ __global__ void __launch_bounds__(kThreadsAtt, 1)
             tmem_st16(myS + 16 * ch, p);
           }
           const float mx = max3(max3(mx4[0], mx4[1], mx4[2]), mx4[3], mx4[3]);
-          const bool move = mine && !((mx - m) * a.c <= 8.f) && m == m;
+          const bool move = mine && mx != m && !((mx - m) * a.c <= 8.f) && m == m;
           if (!__any_sync(0xffffffffu, move)) break;
           const float fix = move ? ex2((m - mx) * a.c) : 1.f;
 #pragma unroll 1

@@ -255,6 +255,26 @@ def test_attention_later_tokens_never_reach_a_query(hq, hk, dtype):
     assert torch.equal(got[:at], clean[:at]) and bool(got[at:].isnan().all())
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("at,value", [((0, 140), -math.inf), ((0, 1), -math.inf), ((5, 6), math.inf), ((200, 201), math.inf),
+                                      ((0, 300), -math.inf), ((130, 260), -math.inf)])
+def test_attention_infinite_scores(at, value, dtype, causal):
+    """Keys whose scores are infinite: -inf weighs nothing, also when a whole block or all that a
+    query sees so far is -inf (NaN where it sees nothing else), and +inf makes NaN."""
+    pwp = _pwp()
+    lens, d = [300], 64
+    q, k, v, cu = att_case(lens, 2, 1, d, dtype, 43)
+    q[:, 0, 0], q[:, 1, 0] = 1.0, -1.0
+    bad = k.clone()
+    bad[at[0]:at[1], 0, 0] = value
+    with np.errstate(invalid="ignore"):
+        want, size = F.attention(np64(q), np64(bad), np64(v), lens, causal, spread=True)
+        k[at[0]:at[1], 0, 0] = 0.0
+        tol = att_tol(q, k, lens, 2, 1, d, want, size, dtype)
+        close(pwp.attention(q, bad, v, cu, causal=causal), want, tol)
+
+
 def test_attention_bad_offsets_are_reported():
     torch, pwp = _torch(), _pwp()
     q, k, v, _ = att_case([100], 2, 1, 64, "bf16", 41)
