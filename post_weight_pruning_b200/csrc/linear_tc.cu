@@ -189,7 +189,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
   uint64_t* afull = empty + P_STAGES;
   uint64_t* aempty = afull + 2;                                                    // the leader's are used
   uint64_t* drain = aempty + 2;
-  __shared__ uint32_t tmem_slot;
+  uint64_t* peer = drain + 1;                                                      // the other CTA's copies are all issued
+  __shared__ uint32_t tmem_slot, peer_steps;
   __shared__ int abort_flag;
   volatile int* abortp = &abort_flag;
 
@@ -209,6 +210,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
       mbar_init(&aempty[a], 2 * P_EPI_WARPS);
     }
     mbar_init(drain, 1);
+    mbar_init(peer, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     abort_flag = 0;
   }
@@ -232,38 +234,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
       const uint32_t sbase = smem_u32(smem);
       const uint32_t bar0 = map_rank(smem_u32(&full[0]), 0);
       uint32_t s = 0, phase = 0, filled = 0;      // next stage, its phase; stages ever filled (capped)
+      uint32_t steps = 0;                         // steps of k loaded
       bool ok = true;
-      for (int t = first; t < tiles && ok; t += pairs) {
-        int m, c;
+      int t = first, kt = 0, m, c;
+      auto load = [&](const CUtensorMap* bmap, int y, int yb) {
+        if (rank == 0) mbar_expect_tx(&full[s], 2 * P_STAGE_BYTES);
+        const uint32_t dst = sbase + s * P_STAGE_BYTES, bar = bar0 + s * 8u;
+        tma_load_pair(dst, &xmap, bar, kt * TK, y);
+        tma_load_pair(dst + P_ROWS * ROW_BYTES, bmap, bar, kt * TK, yb);
+        ++steps;
+        if (++s == P_STAGES) {
+          s = 0;
+          phase ^= 1u;
+        }
+      };
+      const CUtensorMap* bmap = GATED && rank ? &umap : &wmap;
+      while (t < tiles) {
         pair_tile(t, mt, nt, m, c);
         const int y = m * 2 * P_ROWS + (int)rank * P_ROWS;
-        const CUtensorMap* bmap = GATED && rank ? &umap : &wmap;
         const int yb = GATED ? c * NT : c * NT + (int)rank * P_ROWS;
-        for (int kt = 0; kt < nk; ++kt) {
+        for (; kt < nk; ++kt) {
           if (filled < P_STAGES) {
             ++filled;
           } else if (!mbar_wait(&empty[s], phase ^ 1u, abortp, spin)) {
             ok = false;
             break;
           }
-          if (rank == 0) mbar_expect_tx(&full[s], 2 * P_STAGE_BYTES);
-          const uint32_t dst = sbase + s * P_STAGE_BYTES, bar = bar0 + s * 8u;
-          tma_load_pair(dst, &xmap, bar, kt * TK, y);
-          tma_load_pair(dst + P_ROWS * ROW_BYTES, bmap, bar, kt * TK, yb);
-          if (++s == P_STAGES) {
-            s = 0;
-            phase ^= 1u;
-          }
+          load(bmap, y, yb);
         }
+        if (!ok) break;
+        kt = 0;
+        t += pairs;
       }
       if (!ok) *abortp = 1;
-      // both CTAs' copies land before either leaves: they are counted by the leader's barriers
-      if (rank == 0)
+      // Both CTAs' copies land before either leaves.  They are counted by the leader's barriers,
+      // which complete only when both CTAs have loaded a stage: one that gave up a wait the
+      // other did not loads as far as the other (which saw those stages free).
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(smem_u32(&peer_steps), rank ^ 1)), "r"(steps)
+                   : "memory");
+      remote_arrive(map_rank(smem_u32(peer), rank ^ 1));
+      bool met = false;
+      for (int i = 0; i < 4 && !met; ++i) met = mbar_wait(peer, 0, kDrainLimit);   // the other's own waits come before
+      asm volatile("fence.acq_rel.cluster;" ::: "memory");
+      while (met && (int)(*(volatile uint32_t*)&peer_steps - steps) > 0 && t < tiles) {
+        pair_tile(t, mt, nt, m, c);
+        load(bmap, m * 2 * P_ROWS + (int)rank * P_ROWS, GATED ? c * NT : c * NT + (int)rank * P_ROWS);
+        if (++kt == nk) {
+          kt = 0;
+          t += pairs;
+        }
+      }
+      if (rank == 0) {
         for (uint32_t i = 0; i < filled; ++i) {
           if (s == 0) phase ^= 1u;
           s = s == 0 ? P_STAGES - 1 : s - 1;
           mbar_wait(&full[s], phase, kDrainLimit);
         }
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -302,7 +329,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
       }
       if (!ok) *abortp = 1;
       commit_pair(drain);      // every MMA issued has finished before tensor memory is released
-      mbar_wait(drain, 0, kDrainLimit);
     }
     __syncwarp();
   } else {
@@ -402,7 +428,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
 
   fence_before();
   __syncthreads();
-  cluster_sync();       // the peer's copies, MMAs and arrivals on this CTA's barriers are done
+  if (threadIdx.x == 32) mbar_wait(drain, 0, kDrainLimit);   // the MMAs, and their arrivals on this CTA's barriers
+  __syncwarp();
+  cluster_sync();       // the peer's copies and arrivals on this CTA's barriers are done
   fence_after();
   if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * P_ACC_COLS) : "memory");

@@ -462,6 +462,31 @@ def test_waits_that_run_out_are_reported():
         assert torch.equal(call(st), ok) and pwp.read_stats(st).status == 0
 
 
+@pytest.mark.parametrize("gated", [False, True])
+def test_waits_that_run_out_with_many_rows(gated):
+    """The kernel of CTA pairs, several tiles per pair and more steps of k than stages: either CTA
+    may give up first; the rows come out NaN and the next call is right."""
+    torch, pwp = _torch(), _pwp()
+    x, w, u = rnd((16384, 1024), "bf16", 104), rnd((1000, 1024), "bf16", 105), rnd((1000, 1024), "bf16", 106)
+    call = (lambda st=None: pwp.gated_linear(x, w, u, stats=st)) if gated else (lambda st=None: pwp.linear(x, w, stats=st))
+    want = call()
+    torch.cuda.synchronize()
+    for limit in (0, 1, 3):
+        prev = pwp.set_wait_limit(limit)
+        try:
+            st = pwp.new_stats()
+            got = call(st)
+            torch.cuda.synchronize()
+        finally:
+            pwp.set_wait_limit(prev)
+        s = pwp.read_stats(st)
+        assert s.status in ((5,) if limit == 0 else (0, 5)) and (s.status == 0 or s.status_site == 10)
+        wrong = got != want
+        assert bool(got[wrong].isnan().all()) and bool(wrong.any()) == (s.status == 5)
+        st = pwp.new_stats()
+        assert torch.equal(call(st), want) and pwp.read_stats(st).status == 0
+
+
 # ------------------------------------------------------------------- the block
 
 def _block(dtype, heads, kv, width, ff, n, seed=111):
