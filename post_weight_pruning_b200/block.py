@@ -123,14 +123,43 @@ def _check_tensor(t, name, shape, like, dtype=None):
         raise ValueError(f"{name}: elements of the last dimension must be contiguous")
 
 
-def _check_out(t, name, shape, like):
-    """An output given by the caller: no two of its elements in one place."""
+def _overlap(a, b):
+    """Whether the memory of two tensors may have an element in common.  Slices that interleave
+    (heads or columns of one packed buffer) are told apart by their places within a stride
+    they share."""
+    e = a.element_size()
+    dims = [[(st * e, n) for st, n in zip(t.stride(), t.shape) if n != 1] for t in (a, b)]
+    if any(n == 0 for ds in dims for _, n in ds):
+        return False
+    reach = [sum(st * (n - 1) for st, n in ds) + e for ds in dims]
+    gap = b.data_ptr() - a.data_ptr()
+    if gap >= reach[0] or -gap >= reach[1]:
+        return False
+    for pitch in {st for st, _ in dims[0]} & {st for st, _ in dims[1]}:
+        if pitch == 0 or any(st > pitch and st % pitch for ds in dims for st, _ in ds):
+            continue
+        inner = [sum(st * (n - 1) for st, n in ds if st < pitch) + e for ds in dims]
+        if inner[0] <= gap % pitch and gap % pitch + inner[1] <= pitch:
+            return False
+    return True
+
+
+def _check_out(t, name, shape, like, inputs, same=None):
+    """An output given by the caller: no two of its elements in one place, and apart from the
+    inputs, but for the one it may be (`same`, element for element)."""
     _check_tensor(t, name, shape, like)
     reach = 1
     for stride, size in sorted((t.stride(i), t.shape[i]) for i in range(t.dim()) if t.shape[i] > 1):
         if stride < reach:
             raise ValueError(f"{name}: elements overlap (shape {tuple(t.shape)}, strides {t.stride()})")
         reach = stride * size
+    for x in inputs:
+        if x is None or (x is same and x.data_ptr() == t.data_ptr() and
+                         all(n == 1 or i == j for n, i, j in zip(shape, x.stride(), t.stride()))):
+            continue
+        if _overlap(t, x):
+            raise ValueError(f"{name}: overlaps a tensor the call reads or writes")
+    _forward_only(t)
 
 
 def _forward_only(*ts):
@@ -175,8 +204,8 @@ def rms_norm(x, weight=None, *, eps=1e-5, out=None, stream=None):
     _forward_only(x, weight)
     if out is None:
         out = x.new_empty(shape)
-    elif out is not x:
-        _check_out(out, "out", shape, x)
+    else:
+        _check_out(out, "out", shape, x, (x, weight), x)
     if n:
         st = _pwp.lib().pwp_rms_norm(x.data_ptr(), code, n, width, x.stride(0), _ptr(weight), eps, out.data_ptr(),
                                      out.stride(0), _stream_of(x.get_device()))
@@ -251,7 +280,7 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     ``rope_frequencies`` (the first 2 * len(freqs) elements of a head are turned).
     q_weight, k_weight: [d], the head norms' weights, or None for no norm.  layout "half" pairs
     elements i and i + rot/2, "interleaved" 2i and 2i+1.  q_out / k_out: None, tensors of the
-    same shapes, or q / k themselves.  Returns (q_out, k_out)."""
+    same shapes, or q / k themselves; each overlaps nothing else.  Returns (q_out, k_out)."""
     torch = _torch()
     code = _type_code(q, "q", 3)
     n, hq, d = q_shape = q.shape
@@ -278,12 +307,12 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     _forward_only(q, k, q_weight, k_weight)
     if q_out is None:
         q_out = q.new_empty(q_shape)
-    elif q_out is not q:
-        _check_out(q_out, "q_out", q_shape, q)
+    else:
+        _check_out(q_out, "q_out", q_shape, q, (q, k, q_weight, k_weight), q)
     if k_out is None:
         k_out = q.new_empty(k_shape)
-    elif k_out is not k:
-        _check_out(k_out, "k_out", k_shape, q)
+    else:
+        _check_out(k_out, "k_out", k_shape, q, (k, q, q_out, q_weight, k_weight), k)
     if n and hq + hk:
         qs, ks, qos, kos = q.stride(), k.stride(), q_out.stride(), k_out.stride()
         _call("pwp_qk_norm_rope", ROPE_ARGS.pack(
@@ -299,8 +328,8 @@ def attention(q, k, v, cu_seqlens, *, causal=True, scale=None, out=None, stats=N
 
     q: [n, hq, d], k and v: [n, hk, d] (bf16 or fp32, d <= 256, hq a multiple of hk; token and
     head strides free); cu_seqlens: int32 [sequences + 1] on the device: sequence s is rows
-    cu_seqlens[s] to cu_seqlens[s+1].  scale: default 1 / sqrt(d).  Returns out [n, hq, d];
-    rows in no sequence are left as they were (of a fresh output: undefined).  Offsets that
+    cu_seqlens[s] to cu_seqlens[s+1].  scale: default 1 / sqrt(d).  Returns out [n, hq, d]
+    (a tensor of one's own must not overlap q, k or v); rows in no sequence are left as they were (of a fresh output: undefined).  Offsets that
     decrease or leave 0..n end the batch there and set status 1 in `stats` (a ``new_stats``
     record, optional), which also receives a device-side wait that ran out."""
     code = _type_code(q, "q", 3)
@@ -328,7 +357,7 @@ def attention(q, k, v, cu_seqlens, *, causal=True, scale=None, out=None, stats=N
     if out is None:
         out = q.new_empty(q_shape)
     else:
-        _check_out(out, "out", q_shape, q)
+        _check_out(out, "out", q_shape, q, (q, k, v))
     nseq = cu_seqlens.shape[0] - 1
     if n and nseq:
         qs, ks, vs, os = q.stride(), k.stride(), v.stride(), out.stride()
@@ -363,7 +392,7 @@ def _linear(x, w, w_up, bias, bias_up, activation, residual, out, stats, name):
     if out is None:
         out = x.new_empty((rows, n))
     else:
-        _check_out(out, "out", (rows, n), x)
+        _check_out(out, "out", (rows, n), x, (x, w, w_up, bias, bias_up, residual), residual)
     if rows:
         xs, ws = x.stride(0), w.stride(0)
         us = w_up.stride(0) if w_up is not None else 0
@@ -388,7 +417,7 @@ def linear(x, w, *, bias=None, activation="none", residual=None, out=None, stats
     """activation(x w^T + bias) + residual for x [rows, k], w [n, k], bias [n] and residual
     [rows, n] (bf16 or fp32, one type; rows may be strided).  activation: "none", "relu",
     "silu", "gelu" (by the normal distribution) or "gelu_tanh".  out: None or a tensor
-    [rows, n], which may be `residual` itself.  stats: an optional ``new_stats`` record for a
+    [rows, n], which may be `residual` itself but overlap nothing else.  stats: an optional ``new_stats`` record for a
     device-side wait that ran out (without it the rows concerned come out NaN)."""
     return _linear(x, w, None, bias, None, activation, residual, out, stats, "w")
 
@@ -420,7 +449,9 @@ def block_forward(weights, hidden, seq_lens, *, heads, kv_heads=None, freqs=None
 
     Returns (activations, out): {"attn_in", "o_in", "mlp_in", "down_in"}, the inputs of
     the projections as ``FEEDS`` names them (``prune_block``'s activations), and the block's
-    output, residuals included.  stats: an optional ``new_stats`` record."""
+    output, residuals included.  stats: an optional ``new_stats`` record.  The lengths and
+    positions are copied from the host, so the call as a whole cannot be captured into a
+    graph; its operators can."""
     torch = _torch()
     missing = sorted(set(FEEDS) - set(weights))
     if missing:

@@ -164,6 +164,7 @@ def test_operators_refuse_host_tensors():
 CU = torch.zeros(2, dtype=torch.int32)
 POS = torch.zeros(2, dtype=torch.int64)
 FR = torch.zeros(2, dtype=torch.float64)
+POS4 = torch.zeros(4, dtype=torch.int64)
 
 
 @pytest.mark.parametrize("call, err", [
@@ -213,6 +214,49 @@ def test_refusals(fake, call, err):
     with pytest.raises(err):
         call()
     assert not fake.calls
+
+
+X, PACK, BUF = z(4, 8), z(4, 9, 8), z(200)
+
+
+@pytest.mark.parametrize("call", [
+    lambda: pwp.rms_norm(X[:, :4], out=X[:, 2:6]),
+    lambda: pwp.rms_norm(X[:2], out=X[1:3]),
+    lambda: pwp.rms_norm(X, BUF[:8], out=BUF[4:36].view(4, 8)),
+    lambda: pwp.qk_norm_rope(PACK[:, :3], PACK[:, 3:6], POS4, FR, q_out=PACK[:, 3:6]),
+    lambda: pwp.qk_norm_rope(PACK[:, :3], PACK[:, :3], POS4, FR, q_out=PACK[:, :3]),
+    lambda: pwp.qk_norm_rope(PACK[:, :3], PACK[:, 3:6], POS4, FR, q_out=PACK[:, 6:], k_out=PACK[:, 6:]),
+    lambda: pwp.qk_norm_rope(PACK[:, :3], PACK[:, 3:6], POS4, FR, q_out=PACK[:, 2:5]),
+    lambda: pwp.attention(PACK[:, :3], PACK[:, 3:6], PACK[:, 6:], CU, out=PACK[:, :3]),
+    lambda: pwp.attention(PACK[:, :3], PACK[:, 3:6], PACK[:, 6:], CU, out=PACK[:, 5:8]),
+    lambda: pwp.linear(X, z(8, 8), out=X),
+    lambda: pwp.linear(X, z(8, 8), residual=BUF[:32].view(4, 8), out=BUF[8:40].view(4, 8)),
+    lambda: pwp.linear(z(8, 8), X, out=BUF[:32].view(8, 4), bias=BUF[30:34]),
+    lambda: pwp.gated_linear(z(2, 8), z(8, 8), z(8, 8), out=z(2, 8).requires_grad_()),
+])
+def test_outputs_that_overlap_are_refused(fake, call):
+    with pytest.raises(ValueError, match="overlaps|forward pass"):
+        call()
+    assert not fake.calls
+
+
+def test_outputs_beside_their_inputs(fake):
+    q, k, v = PACK[:, :3], PACK[:, 3:6], PACK[:, 6:]
+    pwp.qk_norm_rope(q, k, POS4, FR, q_out=q, k_out=k)
+    pwp.qk_norm_rope(q, k, POS4, FR, q_out=q.view(4, 3, 8), k_out=v)
+    pwp.qk_norm_rope(PACK[:1, :3], PACK[:1, 3:6], POS4[:1], FR, q_out=PACK[:1, :3], k_out=PACK[:1, 3:6])
+    inner = z(4, 3, 2, 8)                                # q and k of a head side by side
+    pwp.qk_norm_rope(inner[:, :, 0], inner[:, :, 1], POS4, FR, q_out=inner[:, :, 0], k_out=inner[:, :, 1])
+    heads = z(6, 4, 8)                                   # head-major
+    pwp.qk_norm_rope(heads[:3].transpose(0, 1), heads[3:].transpose(0, 1), POS4, FR,
+                     q_out=heads[:3].transpose(0, 1), k_out=heads[3:].transpose(0, 1))
+    room = z(4, 12, 8)
+    pwp.attention(room[:, :3], room[:, 3:6], room[:, 6:9], CU, out=room[:, 9:])
+    wide = z(4, 24)
+    pwp.linear(wide[:, :8], z(8, 8), out=wide[:, 8:16], residual=wide[:, 16:])
+    pwp.linear(wide[:, :8], z(8, 8), out=wide[:, 8:16], residual=wide[:, 8:16])
+    pwp.rms_norm(wide[:, :8], out=wide[:, :8])
+    assert len(fake.calls) == 9
 
 
 def test_no_grad_lets_parameters_through(fake):
