@@ -3,7 +3,7 @@
 Tolerances, elementwise and derived from the arithmetic (u = half a step of the output type:
 2^-8 for bf16, 2^-24 for fp32; g = 2^-23, one fp32 step, which bounds an addition rounded
 either way):
-  rms_norm       |y| (u + 2^-8 * 0): the fp32 sum over b terms of one sign is off by less than
+  rms_norm       the fp32 sum over b terms of one sign is off by less than
                  (b / 32 + 16) g (a thread's chain, then a tree), halved by the root, and four
                  more operations follow: u + (b / 64 + 16) g
   qk_norm_rope   the same for the norm; the turn adds |a c| and |b s| each off by 4 g, so
@@ -437,6 +437,82 @@ def test_operators_on_a_stream_of_their_own_and_in_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(kept, want))
+
+
+def test_offsets_past_32_bits():
+    """Rows whose element offsets pass 2^31 (4.6 GB buffer), read and written in place of a copy's."""
+    torch, pwp = _torch(), _pwp()
+    n, pitch, d = 70000, 32768, 64
+    buf = torch.empty((n, pitch), dtype=torch.bfloat16, device="cuda")
+    x, out = buf[:, 8:8 + d], buf[:, 16384:16384 + d]
+    x.copy_(rnd((n, d), "bf16", 120))
+    flat, w = x.contiguous(), rnd((d, d), "bf16", 121, 0.2)
+    pos = torch.arange(n, device="cuda")
+    f, _ = pwp.rope_frequencies(d)
+    cu = torch.tensor([0, 100, n - 3000, n], dtype=torch.int32, device="cuda")
+    heads = lambda t: t.view(n, 1, d)
+    for call in (lambda t, o: pwp.rms_norm(t, out=o), lambda t, o: pwp.linear(t, w, out=o),
+                 lambda t, o: pwp.gated_linear(t, w, w, out=o),
+                 lambda t, o: pwp.qk_norm_rope(heads(t), heads(t), pos, f, q_out=heads(o)),
+                 lambda t, o: pwp.attention(heads(t), heads(t), heads(t), cu[2:], out=heads(o))):
+        want = torch.zeros_like(flat)
+        out.zero_()
+        call(flat, want)
+        call(x, out)
+        assert torch.equal(out, want) and bool(want[n - 3000:].any())
+    want32 = pwp.linear(flat.float(), w.float())
+    del buf, x, out
+    buf = torch.empty((n, pitch), dtype=torch.float32, device="cuda")
+    buf[:, :d] = flat
+    pwp.linear(buf[:, :d], w.float(), out=buf[:, d:2 * d])
+    assert torch.equal(buf[:, d:2 * d], want32)
+
+
+def test_broadcast_inputs():
+    """Stride 0: one row for all rows, one key head for all, one residual row."""
+    torch, pwp = _torch(), _pwp()
+    row, w, r = rnd((1, 256), "bf16", 122), rnd((96, 256), "bf16", 123, 0.1), rnd((1, 96), "bf16", 124)
+    y = pwp.linear(row.expand(40, 256), w, residual=r.expand(40, 96))
+    want = F.linear(np64(row), np64(w), residual=np64(r))
+    tol = U(y.dtype) * np.abs(want) + (256 / 16 + 36) * G * (np.abs(np64(row)) @ np.abs(np64(w)).T + np.abs(np64(r)))
+    close(y, np.repeat(want, 40, 0), np.repeat(tol, 40, 0))
+    y = pwp.linear(rnd((40, 256), "bf16", 125), w[:1].expand(96, 256))
+    assert torch.equal(y, y[:, :1].expand(40, 96))
+    z = pwp.rms_norm(row.expand(5, 256))
+    assert torch.equal(z, pwp.rms_norm(row).expand(5, 256))
+    q, k, v, cu = att_case([150], 4, 1, 64, "bf16", 126)
+    got = pwp.attention(q, k.expand(150, 4, 64), v.expand(150, 4, 64), cu)
+    want, size = F.attention(np64(q), np64(k), np64(v), [150], spread=True)
+    close(got, want, att_tol(q, k, [150], 4, 1, 64, want, size, "bf16"))
+
+
+def test_two_graphs_at_once():
+    """Two captured graphs of calls that take scratch, replayed on two streams beside each other
+    and beside an eager call, several times."""
+    torch, pwp = _torch(), _pwp()
+    xs = [rnd((700, 1001), "bf16", 127 + i) for i in range(3)]
+    w = rnd((300, 1001), "bf16", 130, 0.1)
+    q, k, v, cu = att_case([400, 1, 333], 4, 2, 128, "bf16", 131)
+    run = lambda x: (pwp.linear(x, w, activation="silu"), pwp.rms_norm(x), pwp.attention(q, k, v, cu))
+    want = [run(x) for x in xs]
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for x in xs[:2]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(run(x))
+        graphs.append(g)
+    for _ in range(5):
+        for o in outs:
+            for t in o:
+                t.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        mine = run(xs[2])
+        torch.cuda.synchronize()
+        for got, ref in zip(outs + [mine], want):
+            assert all(torch.equal(a, b) for a, b in zip(got, ref))
 
 
 def test_waits_that_run_out_are_reported():
