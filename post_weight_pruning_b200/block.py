@@ -14,8 +14,6 @@ pass only: an input that requires a gradient is refused while gradients are reco
 from __future__ import annotations
 
 import ctypes
-import functools
-import inspect
 import math
 import struct
 
@@ -47,40 +45,37 @@ SIGNATURES = {
 }
 
 
-_loaded = None
+_loaded = _current_device = None
 
 
 def _torch():
     """torch, imported at the first call (looking it up again costs a small operator's call
     as much as its launch checks)."""
-    global _loaded
+    global _loaded, _current_device
     if _loaded is None:
         _loaded = _pwp._torch()
+        _current_device = _loaded._C._cuda_getDevice
     return _loaded
 
 
 # ------------------------------------------------------------------- argument checks
 
-def _operator(fn):
-    """Run an operator on the device of its first tensor, and on the given stream of that
-    device when there is one."""
-    on_stream = _pwp._on_stream(fn)
-    first = next(iter(inspect.signature(fn).parameters))
+def _away(x, stream):
+    """Whether an operator on `x` has to change the current device or stream first."""
+    try:
+        dev = x.get_device()
+    except AttributeError:
+        raise TypeError(f"tensor expected, got {type(x).__name__}") from None
+    if stream is not None:
+        if dev >= 0 and stream.device_index != dev:
+            raise ValueError(f"stream of device {stream.device_index}, tensors on device {dev}")
+        return True
+    return dev >= 0 and dev != (_current_device or _torch()._C._cuda_getDevice)()
 
-    @functools.wraps(fn)
-    def wrapped(*a, **kw):
-        x = a[0] if a else kw.get(first)
-        try:
-            dev = x.get_device()
-        except AttributeError:
-            raise TypeError(f"{fn.__name__}: {first}: tensor expected, got {type(x).__name__}") from None
-        call = on_stream if "stream" in kw and kw["stream"] is not None else fn
-        cuda = _torch().cuda
-        if dev < 0 or dev == cuda.current_device():
-            return call(*a, **kw)
-        with cuda.device(dev):
-            return call(*a, **kw)
-    return wrapped
+
+def _at(x, stream):
+    """The context of an operator that is away: the given stream, or the device of `x`."""
+    return _pwp._stream_ctx(stream) if stream is not None else _torch().cuda.device(x.device)
 
 
 def _on_gpu(t):
@@ -109,8 +104,7 @@ def _type_code(x, name, dims):
 def _check_tensor(t, name, shape, like, dtype=None):
     """`t` on the device of `like`, of its element type (or `dtype`) and of `shape`, with
     contiguous elements in its last dimension."""
-    if dtype is None:
-        dtype = like.dtype
+    dtype = dtype or like.dtype
     if t.dtype is dtype and t.shape == shape and t.get_device() == like.get_device() and t.stride(-1) == 1:
         return
     if tuple(t.shape) != tuple(shape):
@@ -189,10 +183,12 @@ def _call(name, args, dev):
 
 # ------------------------------------------------------------------- operators
 
-@_operator
 def rms_norm(x, weight=None, *, eps=1e-5, out=None, stream=None):
     """x / sqrt(mean(x^2) + eps) * weight over the rows of x ([n, width], bf16 or fp32;
     rows may be strided).  weight: [width] or None.  out: None, a tensor like x, or x itself."""
+    if _away(x, stream):
+        with _at(x, stream):
+            return rms_norm(x, weight, eps=eps, out=out)
     code = _type_code(x, "x", 2)
     n, width = shape = x.shape
     if width < 1 or width > 65536:
@@ -270,7 +266,6 @@ def rope_frequencies(rot, *, base=10000.0, scaling=None, device="cuda"):
     return torch.from_numpy(np.ascontiguousarray(f, dtype=np.float64)).to(device), factor
 
 
-@_operator
 def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e-5, layout="half", factor=1.0,
                  q_out=None, k_out=None, stream=None):
     """Queries and keys of n tokens, normalised per head and turned by position in one pass.
@@ -281,6 +276,10 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     q_weight, k_weight: [d], the head norms' weights, or None for no norm.  layout "half" pairs
     elements i and i + rot/2, "interleaved" 2i and 2i+1.  q_out / k_out: None, tensors of the
     same shapes, or q / k themselves; each overlaps nothing else.  Returns (q_out, k_out)."""
+    if _away(q, stream):
+        with _at(q, stream):
+            return qk_norm_rope(q, k, positions, freqs, q_weight=q_weight, k_weight=k_weight, eps=eps, layout=layout,
+                                factor=factor, q_out=q_out, k_out=k_out)
     torch = _torch()
     code = _type_code(q, "q", 3)
     n, hq, d = q_shape = q.shape
@@ -322,16 +321,19 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     return q_out, k_out
 
 
-@_operator
 def attention(q, k, v, cu_seqlens, *, causal=True, scale=None, out=None, stats=None, stream=None):
     """Softmax attention within each of the packed sequences.
 
     q: [n, hq, d], k and v: [n, hk, d] (bf16 or fp32, d <= 256, hq a multiple of hk; token and
     head strides free); cu_seqlens: int32 [sequences + 1] on the device: sequence s is rows
     cu_seqlens[s] to cu_seqlens[s+1].  scale: default 1 / sqrt(d).  Returns out [n, hq, d]
-    (a tensor of one's own must not overlap q, k or v); rows in no sequence are left as they were (of a fresh output: undefined).  Offsets that
-    decrease or leave 0..n end the batch there and set status 1 in `stats` (a ``new_stats``
-    record, optional), which also receives a device-side wait that ran out."""
+    (a tensor of one's own must not overlap q, k or v); rows in no sequence are left as they
+    were (of a fresh output: undefined).  Offsets that decrease or leave 0..n end the batch
+    there and set status 1 in `stats` (a ``new_stats`` record, optional), which also receives
+    a device-side wait that ran out."""
+    if _away(q, stream):
+        with _at(q, stream):
+            return attention(q, k, v, cu_seqlens, causal=causal, scale=scale, out=out, stats=stats)
     code = _type_code(q, "q", 3)
     n, hq, d = q_shape = q.shape
     if k.dim() != 3:
@@ -412,22 +414,28 @@ def _linear(x, w, w_up, bias, bias_up, activation, residual, out, stats, name):
     return out
 
 
-@_operator
 def linear(x, w, *, bias=None, activation="none", residual=None, out=None, stats=None, stream=None):
     """activation(x w^T + bias) + residual for x [rows, k], w [n, k], bias [n] and residual
     [rows, n] (bf16 or fp32, one type; rows may be strided).  activation: "none", "relu",
     "silu", "gelu" (by the normal distribution) or "gelu_tanh".  out: None or a tensor
-    [rows, n], which may be `residual` itself but overlap nothing else.  stats: an optional ``new_stats`` record for a
-    device-side wait that ran out (without it the rows concerned come out NaN)."""
+    [rows, n], which may be `residual` itself but overlap nothing else.  stats: an optional
+    ``new_stats`` record for a device-side wait that ran out (without it the rows concerned
+    come out NaN)."""
+    if _away(x, stream):
+        with _at(x, stream):
+            return linear(x, w, bias=bias, activation=activation, residual=residual, out=out, stats=stats)
     return _linear(x, w, None, bias, None, activation, residual, out, stats, "w")
 
 
-@_operator
 def gated_linear(x, w_gate, w_up, *, bias_gate=None, bias_up=None, activation="silu", out=None, stats=None,
                  stream=None):
     """activation(x w_gate^T + bias_gate) * (x w_up^T + bias_up): both projections of a gated
     feed-forward block, the activation and the product in one kernel.  Shapes, types and the
     other arguments as for ``linear``."""
+    if _away(x, stream):
+        with _at(x, stream):
+            return gated_linear(x, w_gate, w_up, bias_gate=bias_gate, bias_up=bias_up, activation=activation, out=out,
+                                stats=stats)
     return _linear(x, w_gate, w_up, bias_gate, bias_up, activation, None, out, stats, "w_gate")
 
 

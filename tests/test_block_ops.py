@@ -259,6 +259,19 @@ def test_outputs_beside_their_inputs(fake):
     assert len(fake.calls) == 9
 
 
+def test_stream_of_another_device_is_refused(fake, monkeypatch):
+    class Stream:
+        device_index = 1
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    for call in (lambda s: pwp.rms_norm(z(2, 4), stream=s), lambda s: pwp.linear(z(2, 4), z(3, 4), stream=s),
+                 lambda s: pwp.gated_linear(z(2, 4), z(3, 4), z(3, 4), stream=s),
+                 lambda s: pwp.attention(z(2, 2, 4), z(2, 2, 4), z(2, 2, 4), CU, stream=s),
+                 lambda s: pwp.qk_norm_rope(z(2, 1, 4), z(2, 1, 4), POS, FR, stream=s)):
+        with pytest.raises(ValueError, match="device"):
+            call(Stream())
+    assert not fake.calls
+
+
 def test_no_grad_lets_parameters_through(fake):
     with torch.no_grad():
         pwp.linear(z(2, 4), z(3, 4).requires_grad_())
