@@ -2,7 +2,8 @@
 hidden states into the activations its layers are pruned with.
 
 ``rms_norm``, ``qk_norm_rope``, ``attention``, ``linear`` and ``gated_linear`` marshal their
-arguments to the C entry points of the same names (include/pwp.h); ``rope_frequencies`` forms
+arguments to the C entry points of the same names (include/pwp.h), the usual calls in C++
+(csrc/fastcall.cpp), all others here; ``rope_frequencies`` forms
 the rotation's frequencies.  ``block_forward`` runs them as a decoder block and returns every
 distinct layer input beside the block's output, and ``prune_decoder_block`` prunes the block
 with those inputs and passes the hidden states through the pruned layers.
@@ -56,6 +57,27 @@ def _torch():
         _loaded = _pwp._torch()
         _current_device = _loaded._C._cuda_getDevice
     return _loaded
+
+
+class _NoFastCalls:
+    """In the place of _fastcall where it is not built: takes no call."""
+    rms_norm = qk_norm_rope = attention = linear = staticmethod(lambda *a: None)
+
+
+_fast = None
+
+
+def _fast_calls():
+    """_fastcall: the usual calls' checks and marshalling in C++ (the same C entry points).  It
+    returns None for what it does not take, which the operators below then check and run."""
+    global _fast
+    if _fast is None:
+        _torch()
+        try:
+            from . import _fastcall as _fast
+        except ImportError:
+            _fast = _NoFastCalls
+    return _fast
 
 
 # ------------------------------------------------------------------- argument checks
@@ -186,6 +208,10 @@ def _call(name, args, dev):
 def rms_norm(x, weight=None, *, eps=1e-5, out=None, stream=None):
     """x / sqrt(mean(x^2) + eps) * weight over the rows of x ([n, width], bf16 or fp32;
     rows may be strided).  weight: [width] or None.  out: None, a tensor like x, or x itself."""
+    if out is None and stream is None:
+        y = (_fast or _fast_calls()).rms_norm(x, weight, eps)
+        if y is not None:
+            return y
     if _away(x, stream):
         with _at(x, stream):
             return rms_norm(x, weight, eps=eps, out=out)
@@ -276,6 +302,11 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     q_weight, k_weight: [d], the head norms' weights, or None for no norm.  layout "half" pairs
     elements i and i + rot/2, "interleaved" 2i and 2i+1.  q_out / k_out: None, tensors of the
     same shapes, or q / k themselves; each overlaps nothing else.  Returns (q_out, k_out)."""
+    if q_out is None and k_out is None and stream is None:
+        y = (_fast or _fast_calls()).qk_norm_rope(q, k, positions, freqs, q_weight, k_weight, eps, LAYOUTS.get(layout),
+                                                  factor)
+        if y is not None:
+            return y
     if _away(q, stream):
         with _at(q, stream):
             return qk_norm_rope(q, k, positions, freqs, q_weight=q_weight, k_weight=k_weight, eps=eps, layout=layout,
@@ -331,6 +362,10 @@ def attention(q, k, v, cu_seqlens, *, causal=True, scale=None, out=None, stats=N
     were (of a fresh output: undefined).  Offsets that decrease or leave 0..n end the batch
     there and set status 1 in `stats` (a ``new_stats`` record, optional), which also receives
     a device-side wait that ran out."""
+    if out is None and stream is None:
+        y = (_fast or _fast_calls()).attention(q, k, v, cu_seqlens, causal, scale, stats)
+        if y is not None:
+            return y
     if _away(q, stream):
         with _at(q, stream):
             return attention(q, k, v, cu_seqlens, causal=causal, scale=scale, out=out, stats=stats)
@@ -421,6 +456,10 @@ def linear(x, w, *, bias=None, activation="none", residual=None, out=None, stats
     [rows, n], which may be `residual` itself but overlap nothing else.  stats: an optional
     ``new_stats`` record for a device-side wait that ran out (without it the rows concerned
     come out NaN)."""
+    if out is None and stream is None:
+        y = (_fast or _fast_calls()).linear(x, w, None, bias, None, ACTIVATIONS.get(activation), residual, stats)
+        if y is not None:
+            return y
     if _away(x, stream):
         with _at(x, stream):
             return linear(x, w, bias=bias, activation=activation, residual=residual, out=out, stats=stats)
@@ -432,6 +471,10 @@ def gated_linear(x, w_gate, w_up, *, bias_gate=None, bias_up=None, activation="s
     """activation(x w_gate^T + bias_gate) * (x w_up^T + bias_up): both projections of a gated
     feed-forward block, the activation and the product in one kernel.  Shapes, types and the
     other arguments as for ``linear``."""
+    if out is None and stream is None:
+        y = (_fast or _fast_calls()).linear(x, w_gate, w_up, bias_gate, bias_up, ACTIVATIONS.get(activation), None, stats)
+        if y is not None:
+            return y
     if _away(x, stream):
         with _at(x, stream):
             return gated_linear(x, w_gate, w_up, bias_gate=bias_gate, bias_up=bias_up, activation=activation, out=out,

@@ -3,22 +3,26 @@
     python -m post_weight_pruning_b200.build          # or build() from Python
 
 Objects go to _build/ at the repository root; the shared library is written next
-to this file so the Python binding finds it.
+to this file so the Python binding finds it.  Where PyTorch is installed, _fastcall.so (the
+forward operators' usual calls, marshalled without the interpreter) is built beside it.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(ROOT, "_build", "obj")
 LIB = os.path.join(HERE, "libpwp.so")
+FASTCALL = os.path.join(HERE, "_fastcall.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + os.path.join(ROOT, "include")]
@@ -47,6 +51,29 @@ def _compile(src, extra, verbose):
     return obj
 
 
+def _build_fastcall(verbose):
+    """g++ against PyTorch's headers and libpwp.so, which is found beside it at run time."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return
+    torch = os.path.dirname(spec.origin)
+    src = os.path.join(CSRC, "fastcall.cpp")
+    header = os.path.join(ROOT, "include", "pwp.h")
+    if os.path.exists(FASTCALL) and os.path.getmtime(FASTCALL) >= max(os.path.getmtime(src), os.path.getmtime(header)):
+        return
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
+    lib = os.path.join(torch, "lib")
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", src, "-o", FASTCALL, *("-I" + p for p in inc), "-L" + HERE,
+           "-l:libpwp.so", "-Wl,-rpath,$ORIGIN", "-L" + lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+
+
 def build(verbose: bool = False, extra=()) -> str:
     os.makedirs(OBJ, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -58,6 +85,7 @@ def build(verbose: bool = False, extra=()) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _build_fastcall(verbose)
     return LIB
 
 

@@ -515,6 +515,72 @@ def test_two_graphs_at_once():
             assert all(torch.equal(a, b) for a, b in zip(got, ref))
 
 
+def test_usual_calls_with_and_without_the_native_marshalling(monkeypatch):
+    """The C++ marshalling takes the usual calls and gives what the Python one gives, bit for bit;
+    what it does not take runs or is refused as before."""
+    torch, pwp = _torch(), _pwp()
+    from post_weight_pruning_b200 import block as B
+    fast, taken = B._fast_calls(), []
+    assert fast is not B._NoFastCalls, "_fastcall.so is not built"
+
+    class Watch:
+        pass
+    for name in ("rms_norm", "qk_norm_rope", "attention", "linear"):
+        def call(*a, f=getattr(fast, name)):
+            y = f(*a)
+            taken.append(y is not None)
+            return y
+        setattr(Watch, name, staticmethod(call))
+    q, k, v, cu = att_case([40, 3], 4, 2, 64, "bf16", 141)
+    pos, (f, s) = torch.arange(43, device="cuda"), pwp.rope_frequencies(32)
+    qw, x, w, u = rnd((64,), "bf16", 144), rnd((43, 96), "bf16", 145), rnd((80, 96), "bf16", 146), rnd((80, 96), "bf16", 147)
+    b, r, odd = rnd((80,), "bf16", 148), rnd((43, 80), "bf16", 149), rnd((900, 201), "bf16", 150)
+    stats = pwp.new_stats()
+    calls = [lambda: pwp.rms_norm(x), lambda: pwp.rms_norm(x[:, :48], w[0, :48], eps=0), lambda: pwp.rms_norm(x.float()),
+             lambda: pwp.rms_norm(x[:1].expand(4, 96)),
+             lambda: pwp.qk_norm_rope(q, k, pos, f, q_weight=qw, layout="interleaved", factor=2.0),
+             lambda: pwp.qk_norm_rope(q.transpose(0, 1).contiguous().transpose(0, 1), k, pos, f[:0]),
+             lambda: pwp.attention(q, k, v, cu), lambda: pwp.attention(q, k, v, cu, causal=False, scale=0.2, stats=stats),
+             lambda: pwp.attention(q.float(), k.float(), v.float(), cu),
+             lambda: pwp.linear(x, w), lambda: pwp.linear(x, w, bias=b, residual=r, activation="gelu", stats=stats),
+             lambda: pwp.linear(odd, odd[:500]), lambda: pwp.linear(x[:, 3:], w[:, 3:]),
+             lambda: pwp.gated_linear(x, w, u, bias_up=b), lambda: pwp.gated_linear(x.float(), w.float(), u.float())]
+    flat = lambda y: y if isinstance(y, tuple) else (y,)
+    for i, call in enumerate(calls):
+        monkeypatch.setattr(B, "_fast", Watch)
+        got = flat(call())
+        assert taken and taken[-1], i
+        monkeypatch.setattr(B, "_fast", B._NoFastCalls)
+        want = flat(call())
+        for g, e in zip(got, want):
+            assert torch.equal(g, e) and g.stride() == e.stride() and g.dtype == e.dtype and g.device == e.device, i
+    assert pwp.read_stats(stats).status == 0
+    monkeypatch.setattr(B, "_fast", Watch)
+    needs = w.clone().requires_grad_()
+    other = torch.zeros(80, device="cuda")
+    for call, err in [(lambda: pwp.rms_norm(x, w), ValueError), (lambda: pwp.rms_norm(x.half()), TypeError),
+                      (lambda: pwp.rms_norm(x, eps=-1.0), ValueError), (lambda: pwp.rms_norm(x.cpu()), ValueError),
+                      (lambda: pwp.rms_norm(x, eps=math.nan), ValueError), (lambda: pwp.rms_norm(None), TypeError),
+                      (lambda: pwp.linear(x, needs), ValueError), (lambda: pwp.linear(x, w, bias=other), TypeError),
+                      (lambda: pwp.linear(x, w, bias=b[:79]), ValueError), (lambda: pwp.linear(x, w.T), ValueError),
+                      (lambda: pwp.linear(x, w, residual=r[:1]), ValueError), (lambda: pwp.linear(x, w, bias=b.cpu()), ValueError),
+                      (lambda: pwp.linear(x, w, activation="tanh"), ValueError), (lambda: pwp.linear(x, w, stats=b), ValueError),
+                      (lambda: pwp.gated_linear(x, w, u[:79]), ValueError),
+                      (lambda: pwp.attention(q, k, v[:, :1], cu), ValueError), (lambda: pwp.attention(q, k, v, cu.long()), TypeError),
+                      (lambda: pwp.attention(q[:, :3], k, v, cu), ValueError), (lambda: pwp.attention(q, k, v, cu, scale=math.inf), ValueError),
+                      (lambda: pwp.qk_norm_rope(q, k, pos[:42], f), ValueError), (lambda: pwp.qk_norm_rope(q, k, pos, f.float()), TypeError),
+                      (lambda: pwp.qk_norm_rope(q, k, pos, f, layout="x"), ValueError),
+                      (lambda: pwp.qk_norm_rope(q, k, pos, torch.cat([f, f, f])), ValueError)]:
+        with pytest.raises(err):
+            call()
+        assert not taken[-1]
+    with torch.no_grad():
+        assert torch.equal(pwp.linear(x, needs), pwp.linear(x, w)) and taken[-1]
+    assert pwp.rms_norm(x[:0]).shape == (0, 96) and not taken[-1]
+    with torch.inference_mode():
+        assert pwp.rms_norm(x).is_inference()
+
+
 def test_waits_that_run_out_are_reported():
     torch, pwp = _torch(), _pwp()
     q, k, v, cu = att_case([200], 2, 1, 128, "bf16", 101)
