@@ -82,7 +82,7 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n) {
 // ---------------------------------------------------------------- epilogue pieces
 
 struct Epilogue {
-  int vec;             // rows of out and residual can be read and written 16 bytes at a time
+  int vec, pairs;      // rows of out and residual can be read and written 16, 4 bytes at a time
   const bf16* bias;
   const bf16* bias_up;
   const bf16* residual;
@@ -449,64 +449,103 @@ struct Skinny {
   int f;               // output columns per tile: rows of W, and for the gated product of W_up
 };
 
-// Adds the ranks' partial sums, part[q][row][feature], of `rows` rows and writes them: a warp per
-// row, VW neighbouring columns a lane.  Branch-free over the ranks (those past the last read its
-// sums again and add nothing).
-template <bool GATED, int ACT>
+// Where a feature's four sums of a group of rows lie among the 128 of the tile: the even and the
+// odd ones of each half apart, so that a lane which reads slots l and 32 + l of a half has two
+// neighbouring features, without bank conflicts.
+__device__ __forceinline__ int slot_of(int feature) {
+  return (feature & 64) + ((feature & 1) << 5) + ((feature & 63) >> 1);
+}
+
+// Adds the ranks' partial sums, part[q][row / 4][slot][row % 4], of `rows` rows and writes them: a
+// warp takes four rows of 64 features (for the gated product of the 64 outputs), a lane two
+// neighbouring ones.  Branch-free over up to Q ranks (those past the last read its sums again
+// and add nothing).  Few warps, so what counts is the instructions of each: pointers step from
+// row to row, and whole groups with 4-byte aligned pairs have a path of their own.
+template <bool GATED, int ACT, int Q>
 __device__ __forceinline__ void finish_rows(const Skinny& g, const Epilogue& ep, const float* part, int per, int row0,
                                             int rows, int c0, int warp, int lane) {
-  constexpr int VW = GATED ? 2 : 4;
-  const int f = VW * lane, c = c0 + f, cols = min(min(g.f - f, VW), g.n - c);
-  if (cols <= 0) return;
-  float b[VW], bu[VW];
+  constexpr int X = GATED ? 4 : 2;
+  const int units = (rows + 3) / 4 * (GATED ? 1 : 2);
+  for (int unit = warp; unit < units; unit += S_THREADS / 32) {
+    const int rg = GATED ? unit : unit >> 1, half = GATED ? 0 : 64 * (unit & 1);
+    const int f = half + 2 * lane, c = c0 + f, cols = min(min(g.f - f, 2), g.n - c);
+    if (cols <= 0) continue;
+    float s[X][4];
+    const float* src = part + (rg * S_FEATURES + half + lane) * 4;
 #pragma unroll
-  for (int i = 0; i < VW; ++i) {
-    b[i] = ep.bias && i < cols ? to_f32(ep.bias[c + i]) : 0.f;
-    bu[i] = GATED && ep.bias_up && i < cols ? to_f32(ep.bias_up[c + i]) : 0.f;
-  }
-  const bool whole = cols == VW;
-  for (int t = warp; t < rows; t += S_THREADS / 32) {
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};      // four columns, or two of each product
+    for (int q = 0; q < Q; ++q) {
 #pragma unroll
-    for (int q = 0; q < S_MAX_CLUSTER; ++q) {
-      const float* src = part + (min(q, g.split - 1) * per + t) * S_FEATURES + f;
-      float4 x;
-      if (GATED) {
-        const float2 x0 = *reinterpret_cast<const float2*>(src), x1 = *reinterpret_cast<const float2*>(src + 64);
-        x = make_float4(x0.x, x0.y, x1.x, x1.y);
-      } else {
-        x = *reinterpret_cast<const float4*>(src);
+      for (int x = 0; x < X; ++x) {
+        const float4 v = *reinterpret_cast<const float4*>(src + 128 * x);
+        const bool on = q < g.split;
+        s[x][0] = (q ? s[x][0] : 0.f) + (on ? v.x : 0.f);
+        s[x][1] = (q ? s[x][1] : 0.f) + (on ? v.y : 0.f);
+        s[x][2] = (q ? s[x][2] : 0.f) + (on ? v.z : 0.f);
+        s[x][3] = (q ? s[x][3] : 0.f) + (on ? v.w : 0.f);
       }
-      sum[0] += q < g.split ? x.x : 0.f;
-      sum[1] += q < g.split ? x.y : 0.f;
-      sum[2] += q < g.split ? x.z : 0.f;
-      sum[3] += q < g.split ? x.w : 0.f;
+      if (q + 1 < g.split) src += per * S_FEATURES;
     }
-    const long long r = row0 + t;
-    const bf16* res = ep.residual ? ep.residual + r * ep.residual_stride + c : nullptr;
-    bf16* o = ep.out + r * ep.out_stride + c;
-    float v[VW];
+    const bool two = cols == 2;
+    if (ep.bias) {
+      const float b0 = to_f32(ep.bias[c]), b1 = two ? to_f32(ep.bias[c + 1]) : 0.f;
 #pragma unroll
-    for (int i = 0; i < VW; ++i) {
-      v[i] = activate(ACT, sum[i] + b[i]);
-      if (GATED) v[i] *= sum[2 + (i & 1)] + bu[i];
-      if (res && i < cols) v[i] += to_f32(res[i]);
+      for (int t = 0; t < 4; ++t) s[0][t] += b0, s[1][t] += b1;
     }
-    if (whole && ((uintptr_t)o & (2 * VW - 1)) == 0) {
-      if (GATED)
-        *reinterpret_cast<uint32_t*>(o) = pack2(v[0], v[1]);
-      else
-        *reinterpret_cast<uint2*>(o) = make_uint2(pack2(v[0], v[1]), pack2(v[VW - 2], v[VW - 1]));
+    if (GATED && ep.bias_up) {
+      const float b0 = to_f32(ep.bias_up[c]), b1 = two ? to_f32(ep.bias_up[c + 1]) : 0.f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) s[X - 2][t] += b0, s[X - 1][t] += b1;
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      s[0][t] = activate(ACT, s[0][t]);
+      s[1][t] = activate(ACT, s[1][t]);
+      if (GATED) s[0][t] *= s[X - 2][t], s[1][t] *= s[X - 1][t];
+    }
+    const long long r = row0 + 4 * rg;
+    bf16* o = ep.out + r * ep.out_stride + c;
+    const bf16* res = ep.residual ? ep.residual + r * ep.residual_stride + c : nullptr;
+    const int left = rows - 4 * rg;
+    if (ep.pairs && two && left >= 4) {
+      if (res) {
+        uint32_t w[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) w[t] = *reinterpret_cast<const uint32_t*>(res + t * ep.residual_stride);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          s[0][t] += __uint_as_float(w[t] << 16);
+          s[1][t] += __uint_as_float(w[t] & 0xffff0000u);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) *reinterpret_cast<uint32_t*>(o + t * ep.out_stride) = pack2(s[0][t], s[1][t]);
     } else {
 #pragma unroll
-      for (int i = 0; i < VW; ++i)
-        if (i < cols) o[i] = from_f32<bf16>(v[i]);
+      for (int t = 0; t < 4; ++t) {
+        if (t >= left) break;
+        if (res) {
+          s[0][t] += to_f32(res[0]);
+          if (two) s[1][t] += to_f32(res[1]);
+          res += ep.residual_stride;
+        }
+        o[0] = from_f32<bf16>(s[0][t]);
+        if (two) o[1] = from_f32<bf16>(s[1][t]);
+        o += ep.out_stride;
+      }
     }
   }
 }
+template <bool GATED, int ACT>
+__device__ __forceinline__ void finish_split(const Skinny& g, const Epilogue& ep, const float* part, int per, int row0,
+                                             int rows, int c0, int warp, int lane) {
+  if (g.split == 1) finish_rows<GATED, ACT, 1>(g, ep, part, per, row0, rows, c0, warp, lane);
+  else if (g.split == 2) finish_rows<GATED, ACT, 2>(g, ep, part, per, row0, rows, c0, warp, lane);
+  else if (g.split <= 4) finish_rows<GATED, ACT, 4>(g, ep, part, per, row0, rows, c0, warp, lane);
+  else finish_rows<GATED, ACT, S_MAX_CLUSTER>(g, ep, part, per, row0, rows, c0, warp, lane);
+}
 
 template <bool GATED>
-__global__ void __launch_bounds__(S_THREADS, 1)
+__global__ void __launch_bounds__(S_THREADS, 2)
     skinny_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
                   const __grid_constant__ CUtensorMap umap, const Skinny g, const Epilogue ep, pwp_stats* st,
                   long long spin) {
@@ -598,14 +637,14 @@ __global__ void __launch_bounds__(S_THREADS, 1)
   fence_after();
 
   // Row t of the tile is finished by CTA t / per, which gets the partial sums of rank q at
-  // part[q][t % per][feature]; lane = feature, so a warp stores 128 consecutive bytes.
+  // part[q][t % per / 4][slot][t % 4]: four rows of a feature are one 16-byte store, a warp's 32
+  // stores two runs of 256 bytes.
   const bool failed_tile = *abortp != 0;
   float* part = reinterpret_cast<float*>(smem);
   const int have = min(g.npad, g.rows - r0);
-  int per = (have + g.split - 1) / g.split;
-  if (per > 16) per = (per + 15) & ~15;      // 16 rows read at once then go to one CTA
+  const int per = ((have + g.split - 1) / g.split + 3) & ~3;
   const int quarter = warp & 3;
-  const uint32_t pbase = smem_u32(part) + (uint32_t)(rank * per * S_FEATURES + quarter * 32 + lane) * 4u;
+  const uint32_t pbase = smem_u32(part) + (uint32_t)(rank * per * S_FEATURES + slot_of(quarter * 32 + lane) * 4) * 4u;
   for (int j = (warp >> 2) * 16; j < have; j += 32) {
     float v[16];
     tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)j, v);
@@ -614,18 +653,15 @@ __global__ void __launch_bounds__(S_THREADS, 1)
       for (int i = 0; i < 16; ++i) v[i] = __int_as_float(0x7fc00000);
     }
     int to = j / per, at = j - to * per;
-    if (at + 16 <= per && j + 16 <= have) {
-      const uint32_t dst = map_rank(pbase + (uint32_t)(at * S_FEATURES) * 4u, (uint32_t)to);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) remote_store(dst + i * S_FEATURES * 4u, v[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (j + i < have) remote_store(map_rank(pbase + (uint32_t)(at * S_FEATURES) * 4u, (uint32_t)to), v[i]);
-        if (++at == per) {
-          at = 0;
-          ++to;
-        }
+    for (int i = 0; i < 16; i += 4) {
+      if (j + i < have)
+        remote_store4(map_rank(pbase + (uint32_t)(at * S_FEATURES) * 4u, (uint32_t)to),
+                      make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+      at += 4;
+      if (at == per) {
+        at = 0;
+        ++to;
       }
     }
   }
@@ -639,11 +675,11 @@ __global__ void __launch_bounds__(S_THREADS, 1)
   const int t0 = rank * per, mine = min(per, have - t0);
   const float* from = part;
   switch (ep.act) {
-    case PWP_ACT_RELU: finish_rows<GATED, PWP_ACT_RELU>(g, ep, from, per, r0 + t0, mine, c0, warp, lane); break;
-    case PWP_ACT_SILU: finish_rows<GATED, PWP_ACT_SILU>(g, ep, from, per, r0 + t0, mine, c0, warp, lane); break;
-    case PWP_ACT_GELU: finish_rows<GATED, PWP_ACT_GELU>(g, ep, from, per, r0 + t0, mine, c0, warp, lane); break;
-    case PWP_ACT_GELU_TANH: finish_rows<GATED, PWP_ACT_GELU_TANH>(g, ep, from, per, r0 + t0, mine, c0, warp, lane); break;
-    default: finish_rows<GATED, PWP_ACT_NONE>(g, ep, from, per, r0 + t0, mine, c0, warp, lane); break;
+    case PWP_ACT_RELU: finish_split<GATED, PWP_ACT_RELU>(g, ep, from, per, r0 + t0, mine, c0, warp, lane); break;
+    case PWP_ACT_SILU: finish_split<GATED, PWP_ACT_SILU>(g, ep, from, per, r0 + t0, mine, c0, warp, lane); break;
+    case PWP_ACT_GELU: finish_split<GATED, PWP_ACT_GELU>(g, ep, from, per, r0 + t0, mine, c0, warp, lane); break;
+    case PWP_ACT_GELU_TANH: finish_split<GATED, PWP_ACT_GELU_TANH>(g, ep, from, per, r0 + t0, mine, c0, warp, lane); break;
+    default: finish_split<GATED, PWP_ACT_NONE>(g, ep, from, per, r0 + t0, mine, c0, warp, lane); break;
   }
 }
 
@@ -692,12 +728,13 @@ cudaError_t run_pair(const pwp_linear_args& a, const Epilogue& ep, cudaStream_t 
 // what clusters leave over in a group of SMs.  (The query counts one CTA of a kernel that
 // holds tensor memory per SM; two run beside each other when their shared memory fits.)
 template <bool GATED>
-int resident_ctas(int c) {
+void resident_ctas(int (&ctas)[S_MAX_CLUSTER + 1]) {
   static std::atomic<int> known[64][S_MAX_CLUSTER + 1];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  int n = known[dev][c].load();
-  if (n == 0) {
+  const bool ok = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64;
+  for (int c = 2; c <= S_MAX_CLUSTER; ++c) {
+    ctas[c] = ok ? known[dev][c].load(std::memory_order_relaxed) : 0;
+    if (!ok || ctas[c]) continue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(c * kNumSM));
     cfg.blockDim = dim3(S_THREADS);
@@ -711,12 +748,11 @@ int resident_ctas(int c) {
     int clusters = 0;
     if (cudaOccupancyMaxActiveClusters(&clusters, skinny_kernel<GATED>, &cfg) != cudaSuccess) {
       cudaGetLastError();
-      return 0;
+      continue;
     }
-    n = clusters * c;
-    known[dev][c].store(n);
+    ctas[c] = clusters * c;
+    known[dev][c].store(ctas[c], std::memory_order_relaxed);
   }
-  return n;
 }
 
 template <bool GATED>
@@ -731,26 +767,54 @@ cudaError_t run_skinny(const pwp_linear_args& a, const Epilogue& ep, cudaStream_
   g.rows = (int)a.rows;
   g.n = a.n;
   g.nk = (a.k + TK - 1) / TK;
-  g.row_tiles = (g.rows + 255) / 256;
-  g.npad = (((g.rows + g.row_tiles - 1) / g.row_tiles) + 15) & ~15;
+  // All CTAs of a split are resident at once: a second round of clusters costs as much as the
+  // first (601 x 4096 x 1000: 17 us split 5 ways, 29 us split 6).
+  int resident[S_MAX_CLUSTER + 1];
+  resident_ctas<GATED>(resident);
+  const int col_tiles = (a.n + F - 1) / F;
+  int split = 1, per_sm = 1;
+  if (g.rows <= 64) {
+    // Bound by the weights' bytes: the largest split.  Up to 64 rows two CTAs fit an SM.
+    g.npad = (g.rows + 15) & ~15;
+    per_sm = 2;
+    for (int c = 2; c <= S_MAX_CLUSTER && c <= g.nk; ++c)
+      if ((long long)col_tiles * c <= 2LL * resident[c]) split = c;
+  } else {
+    // Rows per tile and split of k by a model of the time fitted to stamps of the kernel's phases
+    // (us): copies come at 85 KB an SM; a split costs two barriers of the cluster, and its sums
+    // go through distributed shared memory at 24 KB an SM; finishing 64 rows takes 1.5.
+    float best = 1e30f;
+    for (int most = 256; most >= 64; most -= most > 128 ? 64 : 32) {
+      const int rt = (g.rows + most - 1) / most, npad = ((g.rows + rt - 1) / rt + 15) & ~15, here = npad <= 64 ? 2 : 1;
+      const long long t = (long long)col_tiles * ((g.rows + npad - 1) / npad);
+      for (int c = 1; c <= S_MAX_CLUSTER && c <= g.nk; ++c) {
+        if (c > 1 && t * c > (long long)resident[c] * here) continue;
+        const float on_sm = (float)((t * c + kNumSM - 1) / kNumSM);      // CTAs an SM runs, together or in turn
+        float us = on_sm * ((g.nk + c - 1) / c) * (S_FEATURES + npad) * (ROW_BYTES / 85e3f);
+        us += on_sm * ((npad + c - 1) / c) * (1.5f / 64);
+        if (c > 1) us += 1.8f + on_sm * npad * (c - 1) / c * (S_FEATURES * 4 / 24e3f);
+        if (us < best) {
+          best = us;
+          split = c;
+          per_sm = here;
+          g.npad = npad;
+        }
+      }
+    }
+  }
   g.row_tiles = (g.rows + g.npad - 1) / g.npad;
   g.tmem_cols = 32;
   while (g.tmem_cols < g.npad) g.tmem_cols *= 2;
   const int stage_bytes = (S_FEATURES + g.npad) * ROW_BYTES;
-  // Up to 64 rows the stages of two CTAs fit an SM.
-  const int per_sm = g.npad <= 64 ? 2 : 1;
   const int budget = (per_sm == 2 ? 112 : 224) * 1024 - 1024;
   g.stages = budget / stage_bytes < S_MAX_STAGES ? budget / stage_bytes : S_MAX_STAGES;
-  // The largest split whose CTAs are all resident at once: a second round of clusters costs as
-  // much as the first (601 x 4096 x 1000: 17 us split 5 ways, 29 us split 6).
-  long long tiles = (long long)((a.n + F - 1) / F) * g.row_tiles;
-  int split = 1;
-  for (int c = 2; c <= S_MAX_CLUSTER && c <= g.nk; ++c)
-    if (tiles * c <= resident_ctas<GATED>(c) * per_sm) split = c;
+  long long tiles = (long long)col_tiles * g.row_tiles;
   g.f = F;
   if (split == 1 && per_sm == 2) {
     // As many rounds of CTAs as that takes anyway, with equal shares of the columns.
-    const long long slots = kNumSM * per_sm / g.row_tiles, rounds = (tiles + slots - 1) / slots;
+    long long slots = kNumSM * per_sm / g.row_tiles;
+    if (slots < 1) slots = 1;
+    const long long rounds = (col_tiles + slots - 1) / slots;
     g.f = (int)((a.n + slots * rounds - 1) / (slots * rounds));
     g.f = (g.f + 3) & ~3;
     if (g.f > F) g.f = F;
@@ -759,7 +823,7 @@ cudaError_t run_skinny(const pwp_linear_args& a, const Epilogue& ep, cudaStream_
   g.split = split;
   if (tiles > 0x7fffffffLL / split) return cudaSuccess;
   int smem = g.stages * stage_bytes;
-  const int parts = (g.npad + 16 * g.split) * S_FEATURES * (int)sizeof(float);
+  const int parts = (g.npad + 4 * g.split) * S_FEATURES * (int)sizeof(float);
   if (smem < parts) smem = parts;
   smem += 1024;
   CUtensorMap xm, wm, um;
@@ -858,7 +922,9 @@ cudaError_t launch_linear_tc(const pwp_linear_args& a, cudaStream_t s, bool* use
   const long long os = a.rows > 1 ? a.out_stride : 8, rs = a.rows > 1 ? a.residual_stride : 8;
   const bool vec = (a.n & 7) == 0 && (os & 7) == 0 && ((uintptr_t)a.out_dev & 15) == 0 &&
                    (!a.residual_dev || ((rs & 7) == 0 && ((uintptr_t)a.residual_dev & 15) == 0));
-  const Epilogue ep{vec ? 1 : 0, (const bf16*)a.bias_dev, (const bf16*)a.bias_up_dev, (const bf16*)a.residual_dev, (bf16*)a.out_dev,
+  const bool pairs = (os & 1) == 0 && ((uintptr_t)a.out_dev & 3) == 0 &&
+                     (!a.residual_dev || ((rs & 1) == 0 && ((uintptr_t)a.residual_dev & 3) == 0));
+  const Epilogue ep{vec ? 1 : 0, pairs ? 1 : 0, (const bf16*)a.bias_dev, (const bf16*)a.bias_up_dev, (const bf16*)a.residual_dev, (bf16*)a.out_dev,
                     a.residual_stride, a.out_stride, a.activation};
   const bool gated = a.w_up_dev != nullptr;
   // Too few 256-row tiles to fill the SMs' pairs: split k instead.
