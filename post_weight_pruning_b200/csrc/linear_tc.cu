@@ -781,7 +781,7 @@ cudaError_t run_skinny(const pwp_linear_args& a, const Epilogue& ep, cudaStream_
       if ((long long)col_tiles * c <= 2LL * resident[c]) split = c;
   } else {
     // Rows per tile and split of k by a model of the time fitted to stamps of the kernel's phases
-    // (us): copies come at 85 KB an SM; a split costs two barriers of the cluster, and its sums
+    // (us): copies come at 75 KB an SM; a split costs two barriers of the cluster, and its sums
     // go through distributed shared memory at 24 KB an SM; finishing 64 rows takes 1.5.
     float best = 1e30f;
     for (int most = 256; most >= 64; most -= most > 128 ? 64 : 32) {
@@ -790,7 +790,7 @@ cudaError_t run_skinny(const pwp_linear_args& a, const Epilogue& ep, cudaStream_
       for (int c = 1; c <= S_MAX_CLUSTER && c <= g.nk; ++c) {
         if (c > 1 && t * c > (long long)resident[c] * here) continue;
         const float on_sm = (float)((t * c + kNumSM - 1) / kNumSM);      // CTAs an SM runs, together or in turn
-        float us = on_sm * ((g.nk + c - 1) / c) * (S_FEATURES + npad) * (ROW_BYTES / 85e3f);
+        float us = on_sm * ((g.nk + c - 1) / c) * (S_FEATURES + npad) * (ROW_BYTES / 75e3f);
         us += on_sm * ((npad + c - 1) / c) * (1.5f / 64);
         if (c > 1) us += 1.8f + on_sm * npad * (c - 1) / c * (S_FEATURES * 4 / 24e3f);
         if (us < best) {
@@ -810,15 +810,14 @@ cudaError_t run_skinny(const pwp_linear_args& a, const Epilogue& ep, cudaStream_
   g.stages = budget / stage_bytes < S_MAX_STAGES ? budget / stage_bytes : S_MAX_STAGES;
   long long tiles = (long long)col_tiles * g.row_tiles;
   g.f = F;
-  if (split == 1 && per_sm == 2) {
-    // As many rounds of CTAs as that takes anyway, with equal shares of the columns.
-    long long slots = kNumSM * per_sm / g.row_tiles;
-    if (slots < 1) slots = 1;
-    const long long rounds = (col_tiles + slots - 1) / slots;
+  if (split == 1 && g.rows <= 64) {
+    // As many rounds of CTAs as that takes anyway, with equal shares of the columns.  (With more
+    // rows every share reads too much of x again: 1024^3 in 288 CTAs 11.6 us, in 128 10.4.)
+    const long long slots = kNumSM * per_sm, rounds = (tiles + slots - 1) / slots;
     g.f = (int)((a.n + slots * rounds - 1) / (slots * rounds));
     g.f = (g.f + 3) & ~3;
     if (g.f > F) g.f = F;
-    tiles = (long long)((a.n + g.f - 1) / g.f) * g.row_tiles;
+    tiles = (a.n + g.f - 1) / g.f;
   }
   g.split = split;
   if (tiles > 0x7fffffffLL / split) return cudaSuccess;
