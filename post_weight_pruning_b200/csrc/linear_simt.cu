@@ -214,14 +214,22 @@ __global__ void __launch_bounds__(kThreadsSimt, 2) linear_simt_kernel(const pwp_
   });
 }
 
+long long tiles_of(const pwp_linear_args& a, int bm, int out) {
+  return ((a.rows + bm - 1) / bm) * ((a.n + out - 1) / out);
+}
+// Two CTAs fit an SM; a CTA keeps at least 4 steps of k.
+int split_of(const pwp_linear_args& a, long long tiles) {
+  const int nk = (a.k + BK - 1) / BK;
+  int split = 1;
+  while (split < kMaxSplit && tiles * split * 2 <= 2 * kNumSM && nk >= 8 * split) split *= 2;
+  return split;
+}
+
 template <typename T, bool GATED, int BM>
 cudaError_t launch(const pwp_linear_args& a, cudaStream_t s) {
   constexpr int OUT = GATED ? 64 : 128;
-  const long long tiles = ((a.rows + BM - 1) / BM) * ((a.n + OUT - 1) / OUT);
-  const int nk = (a.k + BK - 1) / BK;
-  // Two CTAs fit an SM; a CTA keeps at least 4 steps of k.
-  int split = 1;
-  while (split < kMaxSplit && tiles * split * 2 <= 2 * kNumSM && nk >= 8 * split) split *= 2;
+  const long long tiles = tiles_of(a, BM, OUT);
+  const int split = split_of(a, tiles);
   if (tiles > 0x7fffffffLL / split) return cudaErrorInvalidValue;
   const int work = 2 * BK * (BM + 4 + BN + 4), sums = (BM + kMaxSplit) * BN;
   const int smem = (int)sizeof(float) * (split > 1 && sums > work ? sums : work);
@@ -254,8 +262,9 @@ cudaError_t launch(const pwp_linear_args& a, cudaStream_t s) {
 
 template <typename T, bool GATED>
 cudaError_t launch_rows(const pwp_linear_args& a, cudaStream_t s) {
-  // 32 rows where more would mostly be padding
-  return a.rows <= 96 ? launch<T, GATED, 32>(a, s) : launch<T, GATED, 128>(a, s);
+  // 32 rows where more would mostly be padding, or leave most SMs without a tile
+  const long long tiles = tiles_of(a, 128, GATED ? 64 : 128);
+  return a.rows <= 96 || tiles * split_of(a, tiles) <= kNumSM / 2 ? launch<T, GATED, 32>(a, s) : launch<T, GATED, 128>(a, s);
 }
 
 }  // namespace

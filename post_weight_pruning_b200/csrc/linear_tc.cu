@@ -856,20 +856,26 @@ cudaError_t run_skinny(const pwp_linear_args& a, const Epilogue& ep, cudaStream_
 
 namespace {
 
-// rows of k values from a stride of `stride` to one of `kp` (a multiple of 8); one 16-byte piece per
-// thread and step.  What lies between k and kp is never read as data.
-__global__ void __launch_bounds__(256) align_rows_kernel(const bf16* __restrict__ src, long long stride, long long rows,
-                                                         int k, int kp, bf16* __restrict__ dst) {
-  const int pieces = kp / 8;
-  const long long total = rows * pieces;
+// Rows of k values from a stride of their own to one of `kp` (a multiple of 8), for up to three
+// operands in one launch (blockIdx.y); one 16-byte piece per thread and step.  What lies between
+// k and kp is never read as data.
+struct AlignRows {
+  const bf16* src[3];
+  bf16* dst[3];
+  long long stride[3], rows[3];
+};
+__global__ void __launch_bounds__(256) align_rows_kernel(const AlignRows a, int k, int kp) {
+  pdl_enter();
+  const int which = blockIdx.y, pieces = kp / 8;
+  const long long total = a.rows[which] * pieces;
   for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += 256LL * gridDim.x) {
     const long long r = i / pieces;
     const int c = (int)(i - r * pieces) * 8;
-    const bf16* p = src + r * stride + c;
+    const bf16* p = a.src[which] + r * a.stride[which] + c;
     uint16_t v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = c + j < k ? *reinterpret_cast<const uint16_t*>(p + j) : (uint16_t)0;
-    *reinterpret_cast<uint4*>(dst + r * kp + c) =
+    *reinterpret_cast<uint4*>(a.dst[which] + r * kp + c) =
         make_uint4(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16, v[4] | (uint32_t)v[5] << 16,
                    v[6] | (uint32_t)v[7] << 16);
   }
@@ -882,10 +888,11 @@ size_t copy_bytes(long long rows, int k) { return ((size_t)rows * ((k + 7) & ~7)
 
 }  // namespace
 
-// Copying costs one more read and write of an operand; below 2^24 multiplications the CUDA
-// cores are done as soon.
+// Copying costs one more launch and one more read and write of an operand.  A small product over
+// a short k is done as soon on the CUDA cores (4 x 33 x 50: 6.7 us, 7.2 with copies); they take
+// longer with k (30 x 101 x 100: 13.5, 7.2; 30 x 1001 x 500: 18.5, 7.3).
 size_t linear_align_bytes(const pwp_linear_args& a) {
-  if (a.type != PWP_BF16 || (double)a.rows * a.k * a.n < (double)(1 << 24)) return 0;
+  if (a.type != PWP_BF16 || (a.k < 64 && (double)a.rows * a.k * a.n < (double)(1 << 24))) return 0;
   size_t n = 0;
   if (misaligned(a.x_dev, a.x_stride, a.rows)) n += copy_bytes(a.rows, a.k);
   if (misaligned(a.w_dev, a.w_stride, a.n)) n += copy_bytes(a.n, a.k);
@@ -897,12 +904,16 @@ size_t linear_align_bytes(const pwp_linear_args& a) {
 cudaError_t launch_linear_align(pwp_linear_args& a, cudaStream_t s) {
   char* ws = (char*)a.ws_dev;
   const int kp = (a.k + 7) & ~7;
+  AlignRows r = {};
+  int count = 0;
+  long long most = 0;
   auto copy = [&](const void*& p, int64_t& stride, long long rows) {
     if (!misaligned(p, stride, rows)) return;
-    const long long blocks = (rows * (kp / 8) + 255) / 256;
-    align_rows_kernel<<<(unsigned)(blocks < 16 * kNumSM ? blocks : 16 * kNumSM), 256, 0, s>>>((const bf16*)p, stride, rows,
-                                                                                            a.k, kp, (bf16*)ws);
-    count_launches(1);
+    r.src[count] = (const bf16*)p;
+    r.dst[count] = (bf16*)ws;
+    r.stride[count] = stride;
+    r.rows[count++] = rows;
+    if (rows > most) most = rows;
     p = ws;
     stride = kp;
     ws += copy_bytes(rows, a.k);
@@ -910,7 +921,11 @@ cudaError_t launch_linear_align(pwp_linear_args& a, cudaStream_t s) {
   copy(a.x_dev, a.x_stride, a.rows);
   copy(a.w_dev, a.w_stride, a.n);
   copy(a.w_up_dev, a.w_up_stride, a.n);
-  return cudaGetLastError();
+  const long long blocks = (most * (kp / 8) + 255) / 256;
+  const cudaError_t e = launch_pdl(align_rows_kernel, dim3((unsigned)(blocks < 16 * kNumSM ? blocks : 16 * kNumSM), (unsigned)count),
+                                   dim3(256), (size_t)0, s, r, a.k, kp);
+  count_launches(1);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 // Declines (used = false) when the tensors do not meet the copies' rules (16-byte aligned
