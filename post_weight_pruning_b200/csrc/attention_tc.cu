@@ -218,7 +218,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 // 2^x of two values on the FMA pipe: x = n + f with n the nearest whole number, f in [-1/2, 1/2],
 // and 2^f by the cubic 1 + f (a + f (b + f c)) of least largest relative error (found by linear
-// programming over 4001 points: 1.02e-4 = 2^-13.3, a sixteenth of a bf16 half step).  The
+// programming over 4001 points: 1.02e-4 = 2^-13.3, a fortieth of a bf16 half step).  The
 // constant term is exactly 1, so x clamped at -127 gives exactly 0 (1's exponent field of 127,
 // less 127).
 __device__ __forceinline__ float2 exp2_poly(float2 x) {

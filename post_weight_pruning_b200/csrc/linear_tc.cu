@@ -17,7 +17,7 @@
 // partial sums straight from tensor memory into the shared memory of the CTA that finishes
 // those rows (stores do not wait for the other side, loads from it would), which adds them
 // in rank order -- no atomics, no workspace.  One row of 4096 x 4096 bf16 weights:
-// 10.3 us (5.1 at the copy rate), 33 rows of two 11008 x 4096: 34.7 us (27.6).
+// 10.4 us (5.1 at the copy rate), 33 rows of two 11008 x 4096: 33.0 us (27.6).
 //
 // Accumulators are fp32; bias, activation, product and residual are applied in fp32 and the
 // result is rounded to bf16 once.  Every wait is bounded: a wait that runs out records
