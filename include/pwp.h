@@ -294,8 +294,8 @@ pwp_status pwp_pack_24(const float* W_hat_dev, const uint8_t* mask_dev, int32_t 
  * output can be passed as they are; no alignment beyond the element's own is needed (16-byte
  * aligned bases and strides take the fast kernels).  type is PWP_BF16 or PWP_FP32, the same
  * for every tensor of a call; sums are fp32 and each output is rounded once to its type.
- * A call with no rows enqueues nothing.  No workspace,
- * but for misaligned operands of pwp_linear.  stats_dev (linear, attention) is
+ * A call with no rows enqueues nothing.  Workspace is
+ * optional: for large batches of pwp_attention and misaligned operands of pwp_linear.  stats_dev (linear, attention) is
  * optional: it receives device-side errors and is not cleared by the call; without it a
  * wait that runs out leaves NaN in the rows it was to write. */
 
@@ -356,8 +356,14 @@ typedef struct {
     int64_t n;
     int32_t nseq, type, hq, hk, d, causal;
     float scale;
+    void* ws_dev;                /* or NULL */
+    size_t ws_bytes;
 } pwp_attention_args;
 pwp_status pwp_attention(const pwp_attention_args* args, void* stream);
+/* Bytes of scratch (256-byte aligned, its own for every call in flight) that let the SMs share
+ * a large batch evenly: a counter of the work taken, cleared by the call.  0 where nothing is
+ * gained; without the scratch the work is divided beforehand.  The results are the same. */
+size_t pwp_attention_workspace_bytes(const pwp_attention_args* args);
 
 /* out = act(x W^T + bias) + residual, or with w_up_dev the gated product
  * out = act(x W^T + bias) * (x W_up^T + bias_up) + residual.

@@ -34,13 +34,14 @@ FEEDS = {"q_proj": "attn_in", "k_proj": "attn_in", "v_proj": "attn_in", "o_proj"
 # pwp_rope_args, pwp_attention_args and pwp_linear_args field by field, packed in one call: a
 # small operator's time is mostly its host side
 ROPE_ARGS = struct.Struct("@4P8q4Pq6i2f")
-ATTENTION_ARGS = struct.Struct("@4P8q2Pq6if4x")
+ATTENTION_ARGS = struct.Struct("@4P8q2Pq6ifPN")
 LINEAR_ARGS = struct.Struct("@7P5qPq4iPN")
 
 SIGNATURES = {
     "pwp_rms_norm": (_i32, [_vp, _i32, _i64, _i32, _i64, _vp, _f32, _vp, _i64, _vp]),
     "pwp_qk_norm_rope": (_i32, [ctypes.c_char_p, _vp]),
     "pwp_attention": (_i32, [ctypes.c_char_p, _vp]),
+    "pwp_attention_workspace_bytes": (ctypes.c_size_t, [ctypes.c_char_p]),
     "pwp_linear": (_i32, [ctypes.c_char_p, _vp]),
     "pwp_linear_workspace_bytes": (ctypes.c_size_t, [ctypes.c_char_p]),
 }
@@ -398,9 +399,11 @@ def attention(q, k, v, cu_seqlens, *, causal=True, scale=None, out=None, stats=N
     nseq = cu_seqlens.shape[0] - 1
     if n and nseq:
         qs, ks, vs, os = q.stride(), k.stride(), v.stride(), out.stride()
-        _call("pwp_attention", ATTENTION_ARGS.pack(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0],
-            os[1], cu_seqlens.data_ptr(), stats_p, n, nseq, code, hq, hk, d, 1 if causal else 0, scale), q.get_device())
+        args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0],
+                os[1], cu_seqlens.data_ptr(), stats_p, n, nseq, code, hq, hk, d, 1 if causal else 0, scale)
+        need = _pwp.lib().pwp_attention_workspace_bytes(ATTENTION_ARGS.pack(*args, 0, 0))
+        scratch = _torch().empty(need, dtype=_torch().uint8, device=q.device) if need else None
+        _call("pwp_attention", ATTENTION_ARGS.pack(*args, _ptr(scratch), need), q.get_device())
     return out
 
 

@@ -38,6 +38,8 @@
 //
 // Every wait is bounded: one that runs out records PWP_ETIMEOUT and the rows come out NaN;
 // copies and MMAs in flight are waited for before a CTA leaves.
+#include <climits>
+
 #include "block_ops.cuh"
 #include "tc_common.cuh"
 
@@ -70,13 +72,17 @@ struct Att {
   int nseq, hk, group, tq, d, causal;          // tq: tokens per tile
   float c;                                     // scale * log2(e)
   int vec;                                     // 16-byte stores of out are possible
+  int* next;                                   // items taken beyond the first of each CTA, or NULL
 };
 
-// The items of a CTA, in order: the sequences' tile pairs (the last, longest one of a
-// sequence first) with the key heads running fastest.  Warp 0 finds them and hands them to
-// the other roles through a short queue in shared memory.
+// The items: the sequences' tile pairs (the last, longest one of a sequence first) with the key
+// heads running fastest.  A CTA starts with the item of its number and takes the next free one
+// when the copies of its last one are out (a counter in the caller's workspace), or without one
+// every gridDim-th: the heaviest CTA then has 1.05 times the mean work at 16 sequences of 2048
+// tokens, 1.14 at 4, 1.5 at one, against 1.01 to 1.05 with the counter.  Warp 0 finds them and hands them to the other
+// roles through a short queue in shared memory.
 struct Items {
-  int t, s0, base;        // next item; the first sequence of the scan's chunk; tiles before it
+  int t, s0, base;        // last item (-1: none yet); the first sequence of the scan's chunk; tiles before it
 };
 struct __align__(16) Item {
   int begin, len, hk;     // sequence (len < 0: no more items), key head
@@ -90,9 +96,17 @@ struct __align__(16) Item {
 __device__ __forceinline__ bool next_item(const Att& a, Items& it, Item& x, bool& bad) {
   const int lane = threadIdx.x & 31;
   const int per = 2 * a.tq;
+  if (it.t < 0) {
+    it.t = blockIdx.x;
+  } else if (a.next) {
+    int taken = 0;
+    if (lane == 0) taken = atomicAdd(a.next, 1);
+    it.t = gridDim.x + __shfl_sync(0xffffffffu, taken, 0);
+  } else {
+    it.t += gridDim.x;
+  }
   const int tile = it.t / a.hk;
   x.hk = it.t - tile * a.hk;
-  it.t += gridDim.x;
   for (; it.s0 < a.nseq; it.s0 += 32) {
     const int s = it.s0 + lane;
     int b = 0, e = 0;
@@ -266,6 +280,11 @@ struct Bars {
   uint64_t ifull[kQueue], iempty[kQueue];
   Item item[kQueue];
   int vbad[kQueue];                            // item + 1: a non-finite value was taken out of its V
+  // for when a wait runs out: the last items taken, each softmax warp's first one that it did not
+  // finish, and where warp 0 was
+  Item taken[2 * kQueue];
+  int ntaken, done[8];
+  Items it;
   int abort_flag;
   uint32_t tmem;
 };
@@ -299,6 +318,7 @@ __global__ void __launch_bounds__(kThreadsAtt, 1)
     mbar_init(&sb.drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     sb.abort_flag = 0;
+    sb.ntaken = 0;
     for (int i = 0; i < kQueue; ++i) {
       mbar_init(&sb.ifull[i], 1);
       mbar_init(&sb.iempty[i], 11);     // the MMA warp, the fixers and the softmax warps
@@ -319,7 +339,7 @@ __global__ void __launch_bounds__(kThreadsAtt, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {
     // ---------------------------------------------------------------- items and copies
-    Items it{(int)blockIdx.x, 0, 0};
+    Items it{-1, 0, 0};
     Ring<C::SLOTS> rg;
     Ring<kQueue> iq;
     uint32_t filled = 0, items = 0, qn[2] = {0, 0};       // slots ever filled (capped), items, q tiles so far
@@ -329,7 +349,12 @@ __global__ void __launch_bounds__(kThreadsAtt, 1)
       Item x;
       more = next_item(a, it, x, bad);
       if (elected()) {
-        if (!more) x.len = -1;
+        if (!more) {
+          x.len = -1;
+        } else {
+          sb.taken[items % (2 * kQueue)] = x;
+          sb.ntaken = items + 1;
+        }
         if (items >= kQueue) ok = mbar_wait(&sb.iempty[iq.slot], iq.phase ^ 1u, abortp, spin);
         if (ok) {
           sb.item[iq.slot] = x;
@@ -371,6 +396,7 @@ __global__ void __launch_bounds__(kThreadsAtt, 1)
       }
       for (int w = 0; w < 2; ++w)
         if (qn[w]) mbar_wait(&sb.qfull[w], (qn[w] - 1) & 1, kDrainLimit);
+      sb.it = it;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -665,21 +691,11 @@ __global__ void __launch_bounds__(kThreadsAtt, 1)
       iq.step();
       ++item;
     }
-    if (!ok) {
-      // gave up: this item's rows and all later ones come out NaN
-      if (lane == 0) {
+    if (lane == 0) {
+      sb.done[warp - 4] = ok ? INT_MAX : item;
+      if (!ok) {
         *abortp = 1;
         if (a.st) set_error(a.st, PWP_ETIMEOUT, kSiteAttention);
-      }
-      __syncwarp();
-      Items it{(int)blockIdx.x, 0, 0};
-      Item x;
-      bool bad = false;
-      for (int i = 0; next_item(a, it, x, bad); ++i) {
-        const int tok = x.tok + w * a.tq + tok_in;
-        if (i < item || tok_in >= a.tq || tok >= x.len) continue;
-        bf16* out = a.out + (long long)(x.begin + tok) * a.os0 + (long long)(x.hk * a.group + head_in) * a.os1;
-        for (int c = 0; c < a.d; ++c) out[c] = from_f32<bf16>(__int_as_float(0x7fc00000));
       }
     }
   }
@@ -688,6 +704,33 @@ __global__ void __launch_bounds__(kThreadsAtt, 1)
   __syncthreads();
   fence_after();
   if (warp == 1) tmem_free(tmem, 512);
+  if (*abortp) {
+    // A wait ran out: the rows of the items taken and not finished come out NaN, and those of the
+    // items that are left.
+    const int w = (warp - 4) >> 2, row = (warp & 3) * 32 + lane, tok_in = row / a.group, head_in = row - tok_in * a.group;
+    auto fail = [&](const Item& x) {
+      const int tok = x.tok + w * a.tq + tok_in;
+      if (tok_in >= a.tq || tok >= x.len) return;
+      bf16* out = a.out + (long long)(x.begin + tok) * a.os0 + (long long)(x.hk * a.group + head_in) * a.os1;
+      for (int c = 0; c < a.d; ++c) out[c] = from_f32<bf16>(__int_as_float(0x7fc00000));
+    };
+    if (warp >= 4)
+      for (int i = sb.done[warp - 4]; i < sb.ntaken; ++i) fail(sb.taken[i % (2 * kQueue)]);
+    Items it = sb.it;
+    while (true) {
+      __syncthreads();
+      if (warp == 0) {
+        Item x;
+        bool bad = false;
+        if (!next_item(a, it, x, bad)) x.len = -1;
+        if (lane == 0) sb.item[0] = x;
+      }
+      __syncthreads();
+      const Item x = sb.item[0];
+      if (x.len < 0) break;
+      if (warp >= 4) fail(x);
+    }
+  }
 }
 
 // [n][heads][d] bf16 as a tensor of {d, inner heads, outer heads, n}; false when the copies
@@ -720,6 +763,12 @@ bool make_map(CUtensorMap* map, const void* p, int d, int inner, int outer, long
   return r == CUDA_SUCCESS;
 }
 
+// At most this many items: a sequence's last tile pair may be partly filled.
+long long most_items(const pwp_attention_args& a) {
+  return (a.n / (2 * (128 / (a.hq / a.hk))) + a.nseq) * (long long)a.hk;
+}
+constexpr size_t kAttentionWorkspace = 256;
+
 template <int D>
 cudaError_t run(const pwp_attention_args& a, cudaStream_t s, bool* used) {
   const int group = a.hq / a.hk, tq = 128 / group;
@@ -743,6 +792,7 @@ cudaError_t run(const pwp_attention_args& a, cudaStream_t s, bool* used) {
   x.os1 = a.out_stride[1];
   x.vs0 = a.v_stride[0];
   x.vs1 = a.v_stride[1];
+  x.next = nullptr;
   x.nseq = a.nseq;
   x.hk = a.hk;
   x.group = group;
@@ -751,25 +801,50 @@ cudaError_t run(const pwp_attention_args& a, cudaStream_t s, bool* used) {
   x.causal = a.causal != 0;
   x.c = a.scale * 1.4426950408889634f;
   x.vec = ((uintptr_t)a.out_dev & 15) == 0 && (a.out_stride[0] & 7) == 0 && (a.out_stride[1] & 7) == 0;
-  // at most this many items: a sequence's last tile pair may be partly filled
-  const long long items = (a.n / (2 * tq) + a.nseq) * (long long)a.hk;
+  const long long items = most_items(a);
   if (items >= 0x7fffffffLL - kNumSM) return cudaSuccess;
   const int grid = items < kNumSM ? (int)items : kNumSM;
   *used = true;
-  const cudaError_t e = launch_pdl(attention_tc_kernel<D>, dim3(grid), dim3(kThreadsAtt), (size_t)Cfg<D>::SMEM, s, qm, km,
-                                   vm, x, wait_limit());
+  cudaError_t e;
+  if (items <= kNumSM) {
+    e = launch_pdl(attention_tc_kernel<D>, dim3(grid), dim3(kThreadsAtt), (size_t)Cfg<D>::SMEM, s, qm, km, vm, x, wait_limit());
+  } else {
+    // Started after its predecessor: CTAs that start early, on the SMs the predecessor's CTAs leave
+    // first, cost more than the start (16 x 2048 tokens of 32 heads one after another: 765 us,
+    // 618 this way; 1 x 1024: 28.2 us early, 29.1 this way).
+    if (a.ws_dev && a.ws_bytes >= kAttentionWorkspace && attention_workspace(a)) {
+      x.next = (int*)a.ws_dev;
+      e = cudaMemsetAsync(a.ws_dev, 0, sizeof(int), s);
+      if (e != cudaSuccess) return e;
+    }
+    attention_tc_kernel<D><<<grid, kThreadsAtt, Cfg<D>::SMEM, s>>>(qm, km, vm, x, wait_limit());
+    e = cudaSuccess;
+  }
   count_launches(1);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace
 
-// Declines (used = false) for fp32, head sizes past 128 or no multiple of 8, more than 128
-// query heads per key head, a scale that is not positive (the running maximum is taken of the
-// unscaled scores) and tensors the copies cannot take.
+// Not for fp32, head sizes past 128 or no multiple of 8, more than 128 query heads per key head,
+// and a scale that is not positive (the running maximum is taken of the unscaled scores).
+static bool takes(const pwp_attention_args& a) {
+  return a.type == PWP_BF16 && a.d <= 128 && (a.d & 7) == 0 && a.hq / a.hk <= 128 && a.scale > 0.f;
+}
+
+// The counter pays where a CTA has few long items: clearing it and asking it cost 3 us and about
+// a microsecond an item.  With it and without, us: 1 x 2048 tokens of 32 heads 54, 64; 4 x 2048
+// 175, 180; 10 sequences of 0 to 4095 tokens 276, 301; but 16 x 2048 (28 items a CTA) 644, 636,
+// and 64 x 128 71, 67.
+size_t attention_workspace(const pwp_attention_args& a) {
+  const long long items = takes(a) ? most_items(a) : 0;
+  return items > kNumSM && items <= 16 * kNumSM && a.n >= 512LL * a.nseq ? kAttentionWorkspace : 0;
+}
+
+// Declines (used = false) also for tensors the copies cannot take.
 cudaError_t launch_attention_tc(const pwp_attention_args& a, cudaStream_t s, bool* used) {
   *used = false;
-  if (a.type != PWP_BF16 || a.d > 128 || (a.d & 7) || a.hq / a.hk > 128 || !(a.scale > 0.f)) return cudaSuccess;
+  if (!takes(a)) return cudaSuccess;
   return a.d <= 64 ? run<64>(a, s, used) : run<128>(a, s, used);
 }
 

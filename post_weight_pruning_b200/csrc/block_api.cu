@@ -39,14 +39,24 @@ pwp_status pwp_qk_norm_rope(const pwp_rope_args* a, void* stream) {
   return status_of(launch_qk_norm_rope(*a, (cudaStream_t)stream));
 }
 
-pwp_status pwp_attention(const pwp_attention_args* a, void* stream) {
+static bool valid_attention(const pwp_attention_args* a) {
   if (!a || !valid_type(a->type) || a->n < 0 || a->nseq < 0 || a->hq < 1 || a->hk < 1 || a->hq % a->hk != 0 ||
       a->d < 1 || a->d > 256 || a->n > 0x7fffffffLL / a->hq || a->nseq > (1 << 24) || !finite_f(a->scale))
-    return PWP_EINVAL;
+    return false;
   for (int i = 0; i < 2; ++i)
-    if (a->q_stride[i] < 0 || a->k_stride[i] < 0 || a->v_stride[i] < 0 || a->out_stride[i] < 0) return PWP_EINVAL;
+    if (a->q_stride[i] < 0 || a->k_stride[i] < 0 || a->v_stride[i] < 0 || a->out_stride[i] < 0) return false;
+  return true;
+}
+
+size_t pwp_attention_workspace_bytes(const pwp_attention_args* a) {
+  return valid_attention(a) && a->n > 0 && a->nseq > 0 ? attention_workspace(*a) : 0;
+}
+
+pwp_status pwp_attention(const pwp_attention_args* a, void* stream) {
+  if (!valid_attention(a)) return PWP_EINVAL;
   if (a->n == 0 || a->nseq == 0) return PWP_OK;
   if (!a->q_dev || !a->k_dev || !a->v_dev || !a->out_dev || !a->cu_seqlens_dev) return PWP_EINVAL;
+  if (a->ws_dev && ((uintptr_t)a->ws_dev & 255) != 0) return PWP_EWORKSPACE;
   bool used = false;
   const cudaError_t e = launch_attention_tc(*a, (cudaStream_t)stream, &used);
   return status_of(used || e != cudaSuccess ? e : launch_attention_simt(*a, (cudaStream_t)stream));

@@ -127,6 +127,7 @@ cudaError_t launch_rms_norm(const void* x, int type, long long rows, int width, 
                             void* out, long long os, cudaStream_t s);
 cudaError_t launch_qk_norm_rope(const pwp_rope_args& a, cudaStream_t s);
 cudaError_t launch_attention_simt(const pwp_attention_args& a, cudaStream_t s);
+size_t attention_workspace(const pwp_attention_args& a);
 cudaError_t launch_attention_tc(const pwp_attention_args& a, cudaStream_t s, bool* used);
 cudaError_t launch_linear_simt(const pwp_linear_args& a, cudaStream_t s);
 size_t linear_align_bytes(const pwp_linear_args& a);

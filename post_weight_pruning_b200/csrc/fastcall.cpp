@@ -179,6 +179,13 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   r.hk = (int32_t)hk;
   r.d = (int32_t)d;
   r.causal = a[4] == Py_True;
+  at::Tensor scratch;
+  const size_t need = pwp_attention_workspace_bytes(&r);
+  if (need) {
+    scratch = at::detail::empty_cuda({(int64_t)need}, at::kByte, q->device(), c10::nullopt);
+    r.ws_dev = scratch.data_ptr();
+    r.ws_bytes = need;
+  }
   if (pwp_attention(&r, c.stream()) != PWP_OK) Py_RETURN_NONE;
   return THPVariable_Wrap(std::move(out));
   END_HANDLE_TH_ERRORS

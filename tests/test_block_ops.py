@@ -109,7 +109,7 @@ class AttentionArgs(ctypes.Structure):
     _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("out", _vp), ("q_stride", _i64 * 2), ("k_stride", _i64 * 2),
                 ("v_stride", _i64 * 2), ("out_stride", _i64 * 2), ("cu_seqlens", _vp), ("stats", _vp), ("n", _i64),
                 ("nseq", _i32), ("type", _i32), ("hq", _i32), ("hk", _i32), ("d", _i32), ("causal", _i32),
-                ("scale", _f32)]
+                ("scale", _f32), ("ws", _vp), ("ws_bytes", ctypes.c_size_t)]
 
 
 class LinearArgs(ctypes.Structure):
@@ -130,6 +130,8 @@ class _FakeLib:
     def __getattr__(self, name):
         if not name.startswith("pwp_"):
             raise AttributeError(name)
+        if name == "pwp_attention_workspace_bytes":
+            return lambda a: 0
 
         def f(*a):
             self.calls.append((name, [ARGS[name].from_buffer_copy(x) if isinstance(x, bytes) else x for x in a]))
@@ -348,6 +350,31 @@ def test_workspace_bytes_of_misaligned_operands():
     assert need(x_stride=1001, type=1) == 0 and need(k=0) == 0
     a = LinearArgs(x=256, w=256, out=256, rows=2, k=4, n=4, x_stride=4, w_stride=4, out_stride=4, ws=264, ws_bytes=99)
     assert L.pwp_linear(bytes(a), None) == 3
+
+
+def test_large_batches_get_a_counter(fake, monkeypatch):
+    asked = []
+    monkeypatch.setattr(_FakeLib, "pwp_attention_workspace_bytes", lambda self, a: asked.append(a) or 256, raising=False)
+    q, cu = z(5, 2, 8), torch.tensor([0, 5], dtype=torch.int32)
+    pwp.attention(q, q, q, cu)
+    a = fake.calls[-1][1][0]
+    assert len(asked) == 1 and a.ws and a.ws_bytes == 256
+
+
+def test_workspace_bytes_of_attention():
+    L = pwp.lib()
+
+    def need(**kw):
+        a = AttentionArgs(q=256, k=256, v=256, out=256, cu_seqlens=256, n=2048, nseq=1, hq=32, hk=32, d=128, scale=0.1)
+        for key, val in kw.items():
+            setattr(a, key, val)
+        return L.pwp_attention_workspace_bytes(bytes(a))
+    assert need() == 256                                    # 8 or 9 tile pairs of 32 heads
+    assert need(n=700) == 0 and need(n=0) == 0              # one round of work
+    assert need(n=32768, nseq=16) == 0 and need(nseq=5) == 0      # many rounds, short sequences
+    assert need(type=1) == 0 and need(d=136) == 0 and need(d=0) == 0 and need(scale=-1.0) == 0
+    a = AttentionArgs(q=256, k=256, v=256, out=256, cu_seqlens=256, n=8, nseq=1, hq=1, hk=1, d=8, scale=1.0, ws=264, ws_bytes=256)
+    assert L.pwp_attention(bytes(a), None) == 3
 
 
 def test_block_forward_refusals(fake):

@@ -275,6 +275,58 @@ def test_attention_infinite_scores(at, value, dtype, causal):
         close(pwp.attention(q, bad, v, cu, causal=causal), want, tol)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_several_rounds_of_work(causal):
+    """More work than one round of the SMs: with the counter and without (the C entry point given
+    no scratch) the same bits; the rows behind the last sequence stay."""
+    torch, pwp = _torch(), _pwp()
+    from post_weight_pruning_b200 import block as B
+    lens = [700, 0, 1, 333, 1024, 1129, 64, 1700] * 2
+    n, extra = sum(lens), 77
+    q, k, v, cu = att_case(lens, 16, 8, 64, "bf16", 151, extra=extra)
+    out = torch.full_like(q, 7.0)
+    pwp.attention(q, k, v, cu, causal=causal, out=out)
+    assert bool((out[n:] == 7.0).all())
+    again = torch.full_like(q, 7.0)
+    args = B.ATTENTION_ARGS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), again.data_ptr(), *q.stride()[:2], *k.stride()[:2],
+                                 *v.stride()[:2], *again.stride()[:2], cu.data_ptr(), 0, n + extra, len(lens), pwp.BF16, 16, 8, 64,
+                                 int(causal), 0.125, 0, 0)
+    assert pwp.lib().pwp_attention_workspace_bytes(args) == 256
+    assert pwp.lib().pwp_attention(args, torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(out, again)
+    at = 0
+    for length in lens[:8]:                         # each sequence by itself
+        s = slice(at, at + length)
+        if length:
+            alone = pwp.attention(q[s], k[s], v[s], torch.tensor([0, length], dtype=torch.int32, device="cuda"), causal=causal)
+            assert torch.equal(alone, out[s])
+        at += length
+    want, size = F.attention(np64(q[701:1034]), np64(k[701:1034]), np64(v[701:1034]), [333], causal, spread=True)
+    close(out[701:1034], want, att_tol(q, k, lens, 16, 8, 64, want, size, "bf16"))
+
+
+def test_attention_several_rounds_when_waits_run_out():
+    """Every row of the sequences comes out NaN, also those of work that nobody took."""
+    torch, pwp = _torch(), _pwp()
+    lens = [1024] * 8
+    q, k, v, cu = att_case(lens, 16, 8, 64, "bf16", 152, extra=5)
+    want = pwp.attention(q, k, v, cu)
+    torch.cuda.synchronize()
+    for limit in (0, 2):
+        prev = pwp.set_wait_limit(limit)
+        try:
+            st, out = pwp.new_stats(), torch.full_like(q, 7.0)
+            pwp.attention(q, k, v, cu, out=out, stats=st)
+            torch.cuda.synchronize()
+        finally:
+            pwp.set_wait_limit(prev)
+        s = pwp.read_stats(st)
+        assert s.status in ((5,) if limit == 0 else (0, 5)) and bool((out[8192:] == 7.0).all())
+        wrong = out[:8192] != want[:8192]
+        assert bool(out[:8192][wrong].isnan().all()) and bool(wrong.any()) == (s.status == 5)
+        assert torch.equal(pwp.attention(q, k, v, cu)[:8192], want[:8192])
+
+
 def test_attention_bad_offsets_are_reported():
     torch, pwp = _torch(), _pwp()
     q, k, v, _ = att_case([100], 2, 1, 64, "bf16", 41)
