@@ -24,8 +24,8 @@
 // S_w(j) becoming full implies that O_w holds block j-1's product (the MMAs of a thread complete
 // in order), so a softmax thread may rescale its row of O_w without another barrier.
 //
-// What bounds it (16 x 2048 tokens, 32 heads of 128: 0.61 ms causal, 0.95 ms full, 895 and 1155
-// TFLOP/s): a tile's chain of softmax (about 1700 cycles per 128 keys: 1024 of exponentials at
+// What bounds it (16 x 2048 tokens, 32 heads of 128: 0.62 ms causal, 0.95 ms full, 890 and 1155
+// TFLOP/s, back to back for seconds 0.72 ms under the power cap): a tile's chain of softmax (about 1700 cycles per 128 keys: 1024 of exponentials at
 // 16 a cycle and SM, the rest issue and latency), its two MMA groups of 512 and the hand-overs
 // between them, which the other tile fills only in part; the tensor core works two thirds of
 // the time.  The single-thread roles are bound by instruction issue and fetch, so they hold
