@@ -61,7 +61,7 @@ def _torch():
 
 
 class _NoFastCalls:
-    """In the place of _fastcall where it is not built: takes no call."""
+    """In the place of _fastcall where it is not built (or for another PyTorch): takes no call."""
     rms_norm = qk_norm_rope = attention = linear = staticmethod(lambda *a: None)
 
 
@@ -73,9 +73,10 @@ def _fast_calls():
     returns None for what it does not take, which the operators below then check and run."""
     global _fast
     if _fast is None:
-        _torch()
+        torch = _torch()
         try:
-            from . import _fastcall as _fast
+            from . import _fastcall
+            _fast = _fastcall if torch.__version__.split("+")[0] == _fastcall.torch_version else _NoFastCalls
         except ImportError:
             _fast = _NoFastCalls
     return _fast
