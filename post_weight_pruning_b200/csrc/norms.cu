@@ -29,6 +29,7 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_kernel(const T* x, long
                                                                 const T* __restrict__ w, float eps, T* out,
                                                                 long long os) {
   __shared__ float part[kNormThreads / 32];
+  pdl_enter();
   const T* xr = x + (long long)blockIdx.x * xs;
   T* yr = out + (long long)blockIdx.x * os;
   float sum = 0.f;
@@ -104,6 +105,7 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_vec_kernel(const T* x, 
   __shared__ float part[kNormThreads / 32];
   const long long r = (long long)blockIdx.x * (kNormThreads / THREADS) + threadIdx.x / THREADS;
   const int t = threadIdx.x % THREADS;
+  pdl_enter();
   if (r >= rows) return;      // whole warps, and only where a row is a warp's
   const uint4* xr = reinterpret_cast<const uint4*>(x + r * xs);
   uint4 u[VPT];
@@ -162,6 +164,7 @@ __device__ __forceinline__ float2 turn_of(long long position, double f, float fa
 template <typename T>
 __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const pwp_rope_args a) {
   extern __shared__ float smem[];
+  pdl_enter();
   const long long t = blockIdx.x;
   const int half = a.rot / 2, d = a.d;
   float2* cs = reinterpret_cast<float2*>(smem);
@@ -236,6 +239,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 2) rope_vec_kernel(const pwp_
   const int lane = threadIdx.x & 31;
   const long long gw = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);   // this warp among all
   const long long t0 = gw / sp.wpt * sp.tpw;                                       // its first token
+  pdl_enter();
   if (t0 >= a.n) return;
   float2* cs = cs_all + (threadIdx.x >> 5) * (sp.tpw * half);
   const int sub = lane / sp.lph, col = lane - sub * sp.lph;      // head slot of the warp, place in the head
@@ -353,6 +357,16 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 2) rope_vec_kernel(const pwp_
   }
 }
 
+// Grids that the GPU takes at once are scheduled while their predecessor ends (a rotation of 37
+// tokens, one after another: 6.1 us, 4.8 this way; a row's norm 4.2, 3.7); larger ones gain nothing.
+template <typename... KArgs, typename... Args>
+void launch_row_kernel(void (*kernel)(KArgs...), long long grid, int block, size_t smem, cudaStream_t s, Args... args) {
+  if (grid <= 2 * kNumSM)
+    launch_pdl(kernel, dim3((unsigned)grid), dim3(block), smem, s, args...);
+  else
+    kernel<<<(unsigned)grid, block, smem, s>>>(args...);
+}
+
 template <typename T>
 bool aligned16(const void* p, long long stride) {
   return ((uintptr_t)p & 15) == 0 && (stride * (long long)sizeof(T)) % 16 == 0;
@@ -366,9 +380,9 @@ cudaError_t run_rms_norm(const T* x, long long rows, int width, long long xs, co
   const int nv = width / VN;
   count_launches(1);
   if (width % VN == 0 && aligned16<T>(x, xs) && aligned16<T>(out, os) && aligned16<T>(w, 0) && nv <= 8 * kNormThreads) {
-#define PWP_NORM(TH, VPT)                                                                                           \
-  rms_norm_vec_kernel<T, TH, VPT><<<(unsigned)((rows + kNormThreads / TH - 1) / (kNormThreads / TH)), kNormThreads, 0, \
-                                    s>>>(x, xs, rows, nv, w, eps, out, os)
+#define PWP_NORM(TH, VPT)                                                                                         \
+  launch_row_kernel(rms_norm_vec_kernel<T, TH, VPT>, (rows + kNormThreads / TH - 1) / (kNormThreads / TH), kNormThreads, \
+                    0, s, x, xs, rows, nv, w, eps, out, os)
     if (nv <= 32) PWP_NORM(32, 1);
     else if (nv <= 64) PWP_NORM(32, 2);
     else if (nv <= 128) PWP_NORM(32, 4);
@@ -378,7 +392,7 @@ cudaError_t run_rms_norm(const T* x, long long rows, int width, long long xs, co
     else PWP_NORM(256, 8);
 #undef PWP_NORM
   } else {
-    rms_norm_kernel<T><<<(unsigned)rows, kNormThreads, 0, s>>>(x, xs, width, w, eps, out, os);
+    launch_row_kernel(rms_norm_kernel<T>, rows, kNormThreads, 0, s, x, xs, width, w, eps, out, os);
   }
   return cudaGetLastError();
 }
@@ -412,13 +426,13 @@ void launch_rope(const pwp_rope_args& a, cudaStream_t s) {
   sp.wpt = 1;
   while (sp.wpt * kRopeBatch < groups && a.n * sp.wpt < 16 * kNumSM) sp.wpt *= 2;
   const long long warps = (a.n + sp.tpw - 1) / sp.tpw * sp.wpt;
-  const unsigned grid = (unsigned)((warps + kRopeWarps - 1) / kRopeWarps);
+  const long long grid = (warps + kRopeWarps - 1) / kRopeWarps;
   const size_t smem = sizeof(float2) * (size_t)(a.rot / 2) * sp.tpw * kRopeWarps;   // at most 16 KB
   const bool norm = a.q_weight_dev || a.k_weight_dev;
   auto kernel = a.layout == PWP_ROPE_HALF
                     ? (norm ? rope_vec_kernel<T, N, true, true> : rope_vec_kernel<T, N, true, false>)
                     : (norm ? rope_vec_kernel<T, N, false, true> : rope_vec_kernel<T, N, false, false>);
-  kernel<<<grid, 32 * kRopeWarps, smem, s>>>(a, sp);
+  launch_row_kernel(kernel, grid, 32 * kRopeWarps, smem, s, a, sp);
 }
 
 template <typename T>
@@ -433,7 +447,7 @@ cudaError_t run_rope(const pwp_rope_args& a, cudaStream_t s) {
     launch_rope<T, 2>(a, s);
   } else {
     const size_t smem = sizeof(float) * (size_t)(a.rot + kRopeWarps * a.d);   // at most 36 KB (d <= 1024)
-    rope_kernel<T><<<(unsigned)a.n, 32 * kRopeWarps, smem, s>>>(a);
+    launch_row_kernel(rope_kernel<T>, a.n, 32 * kRopeWarps, smem, s, a);
   }
   return cudaGetLastError();
 }
