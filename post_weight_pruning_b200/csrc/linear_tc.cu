@@ -120,19 +120,6 @@ __device__ __forceinline__ void add32(float (&v)[32], const bf16* p, int avail) 
       if (i < avail) v[i] += to_f32(p[i]);
   }
 }
-__device__ __forceinline__ void store32(bf16* p, const float (&v)[32], int avail) {
-  if (avail >= 32 && ((uintptr_t)p & 15) == 0) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      *reinterpret_cast<uint4*>(p + 8 * q) =
-          make_uint4(pack2(v[8 * q], v[8 * q + 1]), pack2(v[8 * q + 2], v[8 * q + 3]),
-                     pack2(v[8 * q + 4], v[8 * q + 5]), pack2(v[8 * q + 6], v[8 * q + 7]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < avail) p[i] = from_f32<bf16>(v[i]);
-  }
-}
 // One switch per 32 values, not per value.
 __device__ __forceinline__ void activate32(int act, float (&v)[32]) {
   switch (act) {
@@ -174,6 +161,11 @@ __device__ __forceinline__ void pair_tile(int t, int mt, int nt, int& m, int& n)
   const int rows = min(P_GROUP, mt - g * P_GROUP);
   n = r / rows;
   m = g * P_GROUP + (r - n * rows);
+}
+
+// Two neighbouring columns of a row in a warp's 32 x 32 tile of outputs (see the epilogue).
+__device__ __forceinline__ uint8_t* turn_at(uint8_t* turn, int row, int col) {
+  return turn + row * 64 + (((col >> 3) ^ ((row >> 1) & 3)) << 4) + (col & 7) * 2;
 }
 
 template <bool GATED>
@@ -349,7 +341,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
       fence_after();
       int m, c;
       pair_tile(t, mt, nt, m, c);
-      const long long rw = (long long)m * 2 * P_ROWS + rank * P_ROWS + quarter * 32, r = rw + lane;   // warp's, thread's row
+      const long long rw = (long long)m * 2 * P_ROWS + rank * P_ROWS + quarter * 32;      // the warp's first row
       const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(a * P_ACC_COLS);
       uint8_t* turn = turn_all + (warp - 2) * P_TURN;
       // 32 columns at a time.  A thread holds a row, but 32 rows' 16-byte pieces make 32 separate
@@ -357,7 +349,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
       // reads of the residual, eight rows' whole 64 bytes.  Sixteen warps, because each spends
       // most of its time waiting: at 16384 x 128 x 8192, where the epilogue is the bound, plain
       // 108 us with eight warps of 64 columns and 89-96 with these, with erf-GELU 300 and 190-199.
-      const int prow = lane >> 2, pcol = lane & 3;
+      // Rows that are not 16-byte aligned go two at a time, 4 or 2 bytes a store (8000 x 1000 x 300:
+      // 31.5 us with a row per thread, 13.8 this way).
+      const int prow = lane >> 2, pcol = lane & 3, brow = lane >> 4, bcol = 2 * (lane & 15);
 #pragma unroll 1
       for (int ch = part * (NT / 128); ch < (part + 1) * (NT / 128); ++ch) {
         const int c0 = c * NT + ch * 32, avail = n - c0;
@@ -373,6 +367,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
           for (int q = 0; q < 4; ++q) {
             const int z = prow + 8 * q;
             *reinterpret_cast<uint4*>(turn + z * 64 + ((pcol ^ ((z >> 1) & 3)) << 4)) = w[q];
+          }
+          __syncwarp();
+        } else if (ep.residual) {
+          // two rows at a time, a lane two neighbouring columns
+          const bf16* p = ep.residual + (rw + brow) * ep.residual_stride + c0 + bcol;
+#pragma unroll 8
+          for (int q = 0; q < 16; ++q, p += 2 * ep.residual_stride) {
+            uint32_t w = 0;
+            if (rw + brow + 2 * q < rows && bcol < avail) {
+              if (ep.pairs && bcol + 1 < avail) {
+                w = *reinterpret_cast<const uint32_t*>(p);
+              } else {
+                w = *reinterpret_cast<const uint16_t*>(p);
+                if (bcol + 1 < avail) w |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + 1) << 16;
+              }
+            }
+            *reinterpret_cast<uint32_t*>(turn_at(turn, brow + 2 * q, bcol)) = w;
           }
           __syncwarp();
         }
@@ -393,20 +404,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __int_as_float(0x7fc00000);
         }
-        if (ep.vec) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint4* at = reinterpret_cast<uint4*>(turn + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4));
-            if (ep.residual) {
-              float w[8];
-              unpack8(*at, w);
+        for (int q = 0; q < 4; ++q) {
+          uint4* at = reinterpret_cast<uint4*>(turn + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4));
+          if (ep.residual) {
+            float w[8];
+            unpack8(*at, w);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) v[8 * q + j] += w[j];
-            }
-            *at = make_uint4(pack2(v[8 * q], v[8 * q + 1]), pack2(v[8 * q + 2], v[8 * q + 3]),
-                             pack2(v[8 * q + 4], v[8 * q + 5]), pack2(v[8 * q + 6], v[8 * q + 7]));
+            for (int j = 0; j < 8; ++j) v[8 * q + j] += w[j];
           }
-          __syncwarp();
+          *at = make_uint4(pack2(v[8 * q], v[8 * q + 1]), pack2(v[8 * q + 2], v[8 * q + 3]),
+                           pack2(v[8 * q + 4], v[8 * q + 5]), pack2(v[8 * q + 6], v[8 * q + 7]));
+        }
+        __syncwarp();
+        if (ep.vec) {
           bf16* p = ep.out + (rw + prow) * ep.out_stride + c0 + 8 * pcol;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -414,11 +425,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
             const uint4 w = *reinterpret_cast<const uint4*>(turn + z * 64 + ((pcol ^ ((z >> 1) & 3)) << 4));
             if (on && rw + z < rows) *reinterpret_cast<uint4*>(p + 8 * q * ep.out_stride) = w;
           }
-          __syncwarp();
-        } else if (r < rows) {
-          if (ep.residual) add32(v, ep.residual + r * ep.residual_stride + c0, avail);
-          store32(ep.out + r * ep.out_stride + c0, v, avail);
+        } else {
+          bf16* p = ep.out + (rw + brow) * ep.out_stride + c0 + bcol;
+#pragma unroll 8
+          for (int q = 0; q < 16; ++q, p += 2 * ep.out_stride) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(turn_at(turn, brow + 2 * q, bcol));
+            if (rw + brow + 2 * q < rows && bcol < avail) {
+              if (ep.pairs && bcol + 1 < avail) {
+                *reinterpret_cast<uint32_t*>(p) = w;
+              } else {
+                *reinterpret_cast<uint16_t*>(p) = (uint16_t)w;
+                if (bcol + 1 < avail) *reinterpret_cast<uint16_t*>(p + 1) = (uint16_t)(w >> 16);
+              }
+            }
+          }
         }
+        __syncwarp();
       }
       fence_before();
       __syncwarp();
@@ -941,9 +963,13 @@ cudaError_t launch_linear_tc(const pwp_linear_args& a, cudaStream_t s, bool* use
   const Epilogue ep{vec ? 1 : 0, pairs ? 1 : 0, (const bf16*)a.bias_dev, (const bf16*)a.bias_up_dev, (const bf16*)a.residual_dev, (bf16*)a.out_dev,
                     a.residual_stride, a.out_stride, a.activation};
   const bool gated = a.w_up_dev != nullptr;
-  // Too few 256-row tiles to fill the SMs' pairs: split k instead.
+  // Too few tiles of CTA pairs for the SMs: split k instead.  Alone on their SMs the pairs take
+  // about 5.9 + 0.29 us per 64 of k, the other kernel 6.5 + 0.0095 per 64 of k and tile (200 x 4096
+  // x 4096, 16 tiles: 24.3 us in pairs, 16.4; 700 x 2000 x 2000, 24 tiles: 15.3, 13.7; 2048 x 1024 x
+  // 1024, 32 tiles: 10.6, 12.3; gated 600 x 4096 x 2000, 48 tiles: 26.5, 32.9).
   const long long tiles = ((a.rows + 255) / 256) * ((a.n + (gated ? 127 : 255)) / (gated ? 128 : 256));
-  const bool skinny = a.rows <= 128 || tiles <= 48;
+  const int nk = (a.k + TK - 1) / TK;
+  const bool skinny = a.rows <= 128 || (tiles < 40 && (40 - tiles) * nk > 256);
   if (skinny) return gated ? run_skinny<true>(a, ep, s, used) : run_skinny<false>(a, ep, s, used);
   return gated ? run_pair<true>(a, ep, s, used) : run_pair<false>(a, ep, s, used);
 }

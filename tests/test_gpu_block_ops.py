@@ -422,6 +422,35 @@ def test_linear_strides_and_residual_in_place(rows):
         assert torch.equal(rb[:, :off], before[:, :off]) and torch.equal(rb[:, off + n:], before[:, off + n:])
 
 
+@pytest.mark.parametrize("n", [1000, 1001, 1002, 1004, 1028])
+@pytest.mark.parametrize("off", [0, 1, 2])
+def test_linear_many_rows_of_any_alignment(n, off):
+    """Enough rows and columns for the kernel of CTA pairs, output and residual rows aligned to 16, 4
+    or 2 bytes, a last tile partly filled both ways; what lies around the output stays."""
+    torch, pwp = _torch(), _pwp()
+    rows, k = 3001, 136
+    x, w, u = rnd((rows, k), "bf16", 161), rnd((n, k), "bf16", 162, 0.05), rnd((n, k), "bf16", 163, 0.05)
+    b, room = rnd((n,), "bf16", 164), rnd((rows, n + 5), "bf16", 165)
+    r = room[:, off:off + n]
+    before = room.clone()
+    want = F.linear(np64(x), np64(w), np64(b), "relu", np64(r))
+    pre = F.linear(np64(x), np64(w), np64(b))
+    tol = lin_tol(x, w, b, "relu", pre, want, r, "bf16") + G * np.abs(np64(r)) + 2.0 ** -8 * np.abs(want)
+    close(pwp.linear(x, w, bias=b, activation="relu", residual=r), want, tol)
+    pwp.linear(x, w, bias=b, activation="relu", residual=r, out=r)
+    close(r, want, tol)
+    assert torch.equal(room[:, :off], before[:, :off]) and torch.equal(room[:, off + n:], before[:, off + n:])
+    plain = pwp.gated_linear(x, w, u, bias_gate=b)
+    pwp.gated_linear(x, w, u, bias_gate=b, out=r)
+    assert torch.equal(r, plain)
+    up = F.linear(np64(x), np64(u))
+    want = F.gated_linear(np64(x), np64(w), np64(u), np64(b), None, "silu")
+    eg, eu = lin_tol(x, w, b, "silu", pre, want, None, "bf16"), lin_tol(x, u, None, "none", up, want, None, "bf16", 1.0)
+    tol = eg * np.abs(up) + eu * np.abs(F.activation("silu", pre)) + eg * eu + 2 * G * np.abs(want)
+    close(plain, want, tol + 2.0 ** -8 * np.abs(want) + 1e-37)
+    assert torch.equal(room[:, :off], before[:, :off]) and torch.equal(room[:, off + n:], before[:, off + n:])
+
+
 def test_linear_non_finite_rows_stay_theirs():
     torch, pwp = _torch(), _pwp()
     for rows in (40, 600):
