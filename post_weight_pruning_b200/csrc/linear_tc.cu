@@ -828,8 +828,8 @@ cudaError_t run_skinny(const pwp_linear_args& a, const Epilogue& ep, cudaStream_
   g.tmem_cols = 32;
   while (g.tmem_cols < g.npad) g.tmem_cols *= 2;
   const int stage_bytes = (S_FEATURES + g.npad) * ROW_BYTES;
-  const int budget = (per_sm == 2 ? 112 : 224) * 1024 - 1024;
-  g.stages = budget / stage_bytes < S_MAX_STAGES ? budget / stage_bytes : S_MAX_STAGES;
+  const int room = (per_sm == 2 ? 112 : 224) * 1024 - 1024;
+  g.stages = room / stage_bytes < S_MAX_STAGES ? room / stage_bytes : S_MAX_STAGES;
   long long tiles = (long long)col_tiles * g.row_tiles;
   g.f = F;
   if (split == 1 && g.rows <= 64) {
