@@ -162,20 +162,22 @@ def _overlap(a, b):
     return True
 
 
-def _check_out(t, name, shape, like, inputs, same=None):
+def _check_out(t, name, shape, like, others, same=None):
     """An output given by the caller: no two of its elements in one place, and apart from the
-    inputs, but for the one it may be (`same`, element for element)."""
+    `others`, the tensors the call reads or writes elsewhere.  It may be `same`, the tensor whose
+    every element is read where the output's is written, element for element; a tensor given a
+    second time, as one of the others, is read in other places too."""
     _check_tensor(t, name, shape, like)
     reach = 1
     for stride, size in sorted((t.stride(i), t.shape[i]) for i in range(t.dim()) if t.shape[i] > 1):
         if stride < reach:
             raise ValueError(f"{name}: elements overlap (shape {tuple(t.shape)}, strides {t.stride()})")
         reach = stride * size
-    for x in inputs:
-        if x is None or (x is same and x.data_ptr() == t.data_ptr() and
-                         all(n == 1 or i == j for n, i, j in zip(shape, x.stride(), t.stride()))):
-            continue
-        if _overlap(t, x):
+    if same is not None and same.data_ptr() == t.data_ptr() and \
+            all(n == 1 or i == j for n, i, j in zip(shape, same.stride(), t.stride())):
+        same = None
+    for x in (*others, same):
+        if x is not None and _overlap(t, x):
             raise ValueError(f"{name}: overlaps a tensor the call reads or writes")
     _forward_only(t)
 
@@ -229,7 +231,7 @@ def rms_norm(x, weight=None, *, eps=1e-5, out=None, stream=None):
     if out is None:
         out = x.new_empty(shape)
     else:
-        _check_out(out, "out", shape, x, (x, weight), x)
+        _check_out(out, "out", shape, x, (weight,), x)
     if n:
         st = _pwp.lib().pwp_rms_norm(x.data_ptr(), code, n, width, x.stride(0), _ptr(weight), eps, out.data_ptr(),
                                      out.stride(0), _stream_of(x.get_device()))
@@ -340,11 +342,11 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     if q_out is None:
         q_out = q.new_empty(q_shape)
     else:
-        _check_out(q_out, "q_out", q_shape, q, (q, k, q_weight, k_weight), q)
+        _check_out(q_out, "q_out", q_shape, q, (k, q_weight, k_weight), q)
     if k_out is None:
         k_out = q.new_empty(k_shape)
     else:
-        _check_out(k_out, "k_out", k_shape, q, (k, q, q_out, q_weight, k_weight), k)
+        _check_out(k_out, "k_out", k_shape, q, (q, q_out, q_weight, k_weight), k)
     if n and hq + hk:
         qs, ks, qos, kos = q.stride(), k.stride(), q_out.stride(), k_out.stride()
         _call("pwp_qk_norm_rope", ROPE_ARGS.pack(
@@ -433,7 +435,7 @@ def _linear(x, w, w_up, bias, bias_up, activation, residual, out, stats, name):
     if out is None:
         out = x.new_empty((rows, n))
     else:
-        _check_out(out, "out", (rows, n), x, (x, w, w_up, bias, bias_up, residual), residual)
+        _check_out(out, "out", (rows, n), x, (x, w, w_up, bias, bias_up), residual)
     if rows:
         xs, ws = x.stride(0), w.stride(0)
         us = w_up.stride(0) if w_up is not None else 0

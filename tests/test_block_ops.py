@@ -451,3 +451,32 @@ def test_c_entry_points_check_their_arguments():
                dict(freqs=None), dict(eps=-1.0), dict(factor=math.inf)):
         assert rope(**kw) == 1, kw
     assert rope(n=0) == 0 and L.pwp_qk_norm_rope(None, None) == 1
+
+
+# ------------------------------------------------------------------- the same tensor twice
+
+SQ = z(8, 8)
+
+
+@pytest.mark.parametrize("call", [
+    lambda: pwp.linear(SQ, z(8, 8), residual=SQ, out=SQ),              # rows of x that other tiles still read
+    lambda: pwp.linear(z(8, 8), SQ, residual=SQ, out=SQ),
+    lambda: pwp.qk_norm_rope(PACK[:, :3], PACK[:, :3], POS4, FR, q_out=PACK[:, :3], k_out=PACK[:, :3]),
+])
+def test_outputs_over_a_tensor_given_twice_are_refused(fake, call):
+    with pytest.raises(ValueError, match="overlaps"):
+        call()
+    assert not fake.calls
+
+
+def test_queries_given_as_keys_too(fake):
+    """One tensor as q and k: in place it is read and written at once; apart it may be given."""
+    q = z(4, 3, 8)
+    for kw in (dict(q_out=q), dict(k_out=q), dict(q_out=q, k_out=q), dict(q_out=q, k_out=z(4, 3, 8))):
+        with pytest.raises(ValueError, match="overlaps"):
+            pwp.qk_norm_rope(q, q, POS4, FR, **kw)
+    assert not fake.calls
+    pwp.qk_norm_rope(q, q, POS4, FR)
+    pwp.qk_norm_rope(q, q, POS4, FR, q_out=z(4, 3, 8))
+    pwp.linear(SQ, z(8, 8), residual=SQ)
+    assert len(fake.calls) == 3
