@@ -135,10 +135,10 @@ template <typename T, int D>
 cudaError_t launch(const pwp_attention_args& a, cudaStream_t s) {
   constexpr int smem = (int)sizeof(float) * ((QT + 2 * KT) * (D + 4) + QT * (KT + 1));
   static std::atomic<unsigned long long> attr_done{0};
-  if (first_on_device(attr_done)) {
-    cudaError_t e = cudaFuncSetAttribute(attention_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t ready = on_first_use(attr_done, [] {
+    return cudaFuncSetAttribute(attention_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
+  if (ready != cudaSuccess) return ready;
   // no sequence's tiles are known here: an upper bound of their number (a call with bad
   // offsets, overlapping ones among them, may leave sequences out)
   const long long grid = (a.n / QT + a.nseq) * a.hq;

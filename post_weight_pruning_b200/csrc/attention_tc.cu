@@ -778,10 +778,10 @@ cudaError_t run(const pwp_attention_args& a, cudaStream_t s, bool* used) {
       !make_map(&vm, a.v_dev, a.d, 1, a.hk, a.n, a.v_stride, 3, 1, KEYS))
     return cudaSuccess;
   static std::atomic<unsigned long long> attr_done{0};
-  if (first_on_device(attr_done)) {
-    cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t ready = on_first_use(attr_done, [] {
+    return cudaFuncSetAttribute(attention_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+  });
+  if (ready != cudaSuccess) return ready;
   Att x;
   x.cu = a.cu_seqlens_dev;
   x.st = a.stats_dev;

@@ -869,11 +869,12 @@ cudaError_t launch_damp_factor(float* H, int b, float damp, float* g_diag, void*
   float* vs_lo = vs_hi + (size_t)b * NB;
   float* tcw = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(vs_lo + (size_t)b * NB) + 255) & ~(uintptr_t)255);
   static std::atomic<unsigned long long> attr_done{0};
-  if (first_on_device(attr_done)) {
-    cudaFuncSetAttribute(chol_update_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * NB * 132 * 4);
-    cudaFuncSetAttribute(chol_diag_ahead_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         3 * NB * (NB + 1) * 4);
-  }
+  const cudaError_t ready = on_first_use(attr_done, [] {
+    const cudaError_t e = cudaFuncSetAttribute(chol_update_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * NB * 132 * 4);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(chol_diag_ahead_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       3 * NB * (NB + 1) * 4);
+  });
+  if (ready != cudaSuccess) return ready;
   long long nl = 0;
   launch_pdl(damp_kernel, dim3(1), dim3(1024), 0, s, H, b, damp, g_diag, st);
   ++nl;

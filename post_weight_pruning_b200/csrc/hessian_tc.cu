@@ -299,10 +299,10 @@ cudaError_t launch_hessian_tc(const void* X, long long n, int b, float* H, int b
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (cr != CUDA_SUCCESS) return cudaSuccess;
   static std::atomic<unsigned long long> attr_done{0};
-  if (first_on_device(attr_done)) {
-    cudaError_t e = cudaFuncSetAttribute(syrk_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t ready = on_first_use(attr_done, [] {
+    return cudaFuncSetAttribute(syrk_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  });
+  if (ready != cudaSuccess) return ready;
   launch_pdl(syrk_tc_kernel, dim3(tile_count(b)), dim3(kThreads), SMEM_BYTES, s, map, n, b, H, beta, st, wait_limit());
   *used = true;
   return cudaGetLastError();

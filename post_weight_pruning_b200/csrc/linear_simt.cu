@@ -234,11 +234,11 @@ cudaError_t launch(const pwp_linear_args& a, cudaStream_t s) {
   const int work = 2 * BK * (BM + 4 + BN + 4), sums = (BM + kMaxSplit) * BN;
   const int smem = (int)sizeof(float) * (split > 1 && sums > work ? sums : work);
   static std::atomic<unsigned long long> attr_done{0};
-  if (first_on_device(attr_done)) {
-    cudaError_t e = cudaFuncSetAttribute(linear_simt_kernel<T, GATED, BM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sizeof(float) * (sums > work ? sums : work));
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t ready = on_first_use(attr_done, [&] {
+    return cudaFuncSetAttribute(linear_simt_kernel<T, GATED, BM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)sizeof(float) * (sums > work ? sums : work));
+  });
+  if (ready != cudaSuccess) return ready;
   auto vec4 = [](const void* p, long long stride) {
     return ((uintptr_t)p % (4 * sizeof(T))) == 0 && stride % 4 == 0;
   };

@@ -731,10 +731,10 @@ cudaError_t run_pair(const pwp_linear_args& a, const Epilogue& ep, cudaStream_t 
   um = wm;
   if (GATED && !make_map(&um, a.w_up_dev, a.n, a.k, a.w_up_stride, P_ROWS)) return cudaSuccess;
   static std::atomic<unsigned long long> attr_done{0};
-  if (first_on_device(attr_done)) {
-    cudaError_t e = cudaFuncSetAttribute(pair_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t ready = on_first_use(attr_done, [] {
+    return cudaFuncSetAttribute(pair_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM);
+  });
+  if (ready != cudaSuccess) return ready;
   constexpr int NT = GATED ? 128 : 256;
   const long long tiles = ((a.rows + 2 * P_ROWS - 1) / (2 * P_ROWS)) * ((a.n + NT - 1) / NT);
   if (tiles > 0x3fffffffLL) return cudaSuccess;
@@ -780,10 +780,10 @@ void resident_ctas(int (&ctas)[S_MAX_CLUSTER + 1]) {
 template <bool GATED>
 cudaError_t run_skinny(const pwp_linear_args& a, const Epilogue& ep, cudaStream_t s, bool* used) {
   static std::atomic<unsigned long long> attr_done{0};
-  if (first_on_device(attr_done)) {
-    cudaError_t e = cudaFuncSetAttribute(skinny_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t ready = on_first_use(attr_done, [] {
+    return cudaFuncSetAttribute(skinny_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+  });
+  if (ready != cudaSuccess) return ready;
   constexpr int F = GATED ? S_FEATURES / 2 : S_FEATURES;
   Skinny g;
   g.rows = (int)a.rows;

@@ -461,7 +461,7 @@ static cudaError_t prune_init(PruneRun& R, const pwp_config* cfg, int c, int b, 
   R.Zlo = R.pb.Zs + (size_t)c * R.B;
   // tensor-core update: 16-byte rows for TMA (b, B multiples of 4), aligned W and mask
   R.tc_shape = (b % 4) == 0 && (R.B % 4) == 0 && ((uintptr_t)Wout % 16) == 0 && ((uintptr_t)mask % 4) == 0;
-  if (first_on_device(g_attr_done)) {
+  return on_first_use(g_attr_done, [] {
     cudaError_t e0 = cudaFuncSetAttribute(stream_kernel<kWanda>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           kHist1Bins * 4);
     if (e0 == cudaSuccess)
@@ -469,13 +469,9 @@ static cudaError_t prune_init(PruneRun& R, const pwp_config* cfg, int c, int b, 
     int dev = 0, nsm = kNumSM;
     if (e0 == cudaSuccess) e0 = cudaGetDevice(&dev);
     if (e0 == cudaSuccess) e0 = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
-    if (e0 != cudaSuccess) {
-      g_attr_done.fetch_and(~(1ull << (dev & 63)));   // try again on the next call
-      return e0;
-    }
-    g_nsm = nsm;
-  }
-  return cudaSuccess;
+    if (e0 == cudaSuccess) g_nsm = nsm;
+    return e0;
+  });
 }
 
 // Removal target and budget of the layer (over c_budget rows).

@@ -4,21 +4,10 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "../../include/pwp.h"
+#include "first_use.cuh"
 
 namespace pwp {
-
-// True on the first call for the current device with this flag word.  Kernel
-// attributes (dynamic shared memory limits) are per device, so each device of a
-// multi-GPU process sets them once.  Devices past 63 always set them again (harmless).
-inline bool first_on_device(std::atomic<unsigned long long>& done) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return true;
-  const unsigned long long bit = 1ull << dev;
-  return (done.fetch_or(bit) & bit) == 0;
-}
 
 // Programmatic dependent launch.  Kernels of the prune's dependent chains are launched
 // with programmatic stream serialisation, so a kernel's CTAs may be scheduled while its

@@ -263,8 +263,9 @@ cudaError_t launch_no_update(const pwp_config* cfg, const void* W, int wtype, in
   } else {
     const int smem = 2 * b * 4;
     static std::atomic<unsigned long long> attr_done{0};
-    if (first_on_device(attr_done))
-      cudaFuncSetAttribute(row_quota_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * 16384 * 4);
+    on_first_use(attr_done, [] {      // without it the launch fails, and its error is reported
+      return cudaFuncSetAttribute(row_quota_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * 16384 * 4);
+    });
     // as many resident CTAs as shared memory allows: the radix passes are latency-bound
     int per_sm = 2;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, row_quota_kernel, kRowThreads, smem) != cudaSuccess ||

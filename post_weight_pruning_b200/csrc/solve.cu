@@ -479,8 +479,9 @@ void launch_thanos_variant(const float* W, int c, int b, int j, int B, const flo
                            pwp_stats* st, cudaStream_t s) {
   const int smem = kSolveWarps * kPerWarp * 4;
   static std::atomic<unsigned long long> attr_done{0};
-  if (first_on_device(attr_done))
-    cudaFuncSetAttribute(thanos_solve_kernel<NM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  on_first_use(attr_done, [&] {      // without it the launch fails, and its error is reported
+    return cudaFuncSetAttribute(thanos_solve_kernel<NM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
   const int grid = min((c + kSolveWarps - 1) / kSolveWarps, kSolveCtas);
   launch_pdl(thanos_solve_kernel<NM>, dim3(grid), dim3(kSolveWarps * 32), smem, s, W, c, b, j, B, Kt, xnorm, ctl, l2, mask, Zs, nm_n, nm_m,
                                                                gscratch, st);

@@ -418,11 +418,10 @@ cudaError_t launch_variant(const CUtensorMap* maps, int c, int b, int u0, int j,
                            const uint8_t* mask, const float* sc, int hist_end, unsigned int* hist1, Ctl* ctl,
                            Level2 l2, PickArgs pk, pwp_stats* st, cudaStream_t s, int spare_sms, int keep) {
   static std::atomic<unsigned long long> attr_done{0};
-  if (first_on_device(attr_done)) {
-    cudaError_t e = cudaFuncSetAttribute(stream_tc_kernel<SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         SMEM_BYTES);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t ready = on_first_use(attr_done, [] {
+    return cudaFuncSetAttribute(stream_tc_kernel<SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  });
+  if (ready != cudaSuccess) return ready;
   int dev = 0, nsm = kNumSM;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
