@@ -19,13 +19,37 @@ __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-// Activations of pwp_activation in fp32.  For x far below zero e^-x overflows to infinity
-// and x / inf is -0, the limit of x / (1 + e^-x).
+// Phi(-a), a >= 0, of the standard normal distribution to 2^-20 of itself, and past a = 2 to
+// a^2 2^-23: e^(-a^2/2) times a polynomial in t = 1 / (1 + 0.362 a), the form of Hastings
+// (Abramowitz and Stegun, 26.2.17).  The coefficients have the least largest relative error over
+// [0, 13.5] (7.1e-7; found by linear programming over 4000 points).
+__device__ __forceinline__ float normal_tail(float a) {
+  const float t = __fdividef(1.f, fmaf(a, 0.362f, 1.f));
+  float p = fmaf(0.04804705845356076f, t, -0.1803753304984107f);
+  p = fmaf(p, t, 0.17710773021334036f);
+  p = fmaf(p, t, 0.028496550194732795f);
+  p = fmaf(p, t, 0.13955203359788615f);
+  p = fmaf(p, t, 0.14266678446936745f);
+  p = fmaf(p, t, 0.1445055271023927f);
+  return p * t * __expf(-0.5f * a * a);
+}
+
+// Activations of pwp_activation in fp32, for results of type T.  For x far below zero e^-x
+// overflows to infinity and x / inf is -0, the limit of x / (1 + e^-x).
+//
+// erf-GELU: 1 + erf(x / sqrt 2) would cancel below zero (nothing is left from x = -5.8 on), so
+// fp32 takes erfc, and bf16, whose half step is 2^-8, normal_tail: 16384 x 128 x 8192, where the epilogue
+// is the bound, takes 202 us with it, 208 with erff and 392 with erfcf.
+template <typename T>
 __device__ __forceinline__ float activate(int act, float x) {
   switch (act) {
     case PWP_ACT_RELU: return x != x ? x : fmaxf(x, 0.f);
     case PWP_ACT_SILU: return __fdividef(x, 1.f + __expf(-x));
-    case PWP_ACT_GELU: return 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
+    case PWP_ACT_GELU: {
+      if (sizeof(T) == 4) return 0.5f * x * erfcf(x * -0.70710678118654752f);
+      const float q = normal_tail(fabsf(x));
+      return x * (x < 0.f ? q : 1.f - q);
+    }
     case PWP_ACT_GELU_TANH:      // (1 + tanh t) / 2 = 1 / (1 + e^-2t)
       return __fdividef(x, 1.f + __expf(-1.5957691216057308f * (x + 0.044715f * x * x * x)));
     default: return x;

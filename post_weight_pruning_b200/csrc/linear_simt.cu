@@ -62,7 +62,7 @@ __device__ __forceinline__ void finish4(const pwp_linear_args& a, long long r, i
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (c + i < a.n) {
-      v[i] = activate(ACT, v[i] + (bias ? to_f32(bias[c + i]) : 0.f));
+      v[i] = activate<T>(ACT, v[i] + (bias ? to_f32(bias[c + i]) : 0.f));
       if (GATED) v[i] *= u[i] + (bias_up ? to_f32(bias_up[c + i]) : 0.f);
       if (res) v[i] += to_f32(res[c + i]);
     }

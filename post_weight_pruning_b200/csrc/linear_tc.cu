@@ -125,19 +125,19 @@ __device__ __forceinline__ void activate32(int act, float (&v)[32]) {
   switch (act) {
     case PWP_ACT_RELU:
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = activate(PWP_ACT_RELU, v[i]);
+      for (int i = 0; i < 32; ++i) v[i] = activate<bf16>(PWP_ACT_RELU, v[i]);
       break;
     case PWP_ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = activate(PWP_ACT_SILU, v[i]);
+      for (int i = 0; i < 32; ++i) v[i] = activate<bf16>(PWP_ACT_SILU, v[i]);
       break;
     case PWP_ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = activate(PWP_ACT_GELU, v[i]);
+      for (int i = 0; i < 32; ++i) v[i] = activate<bf16>(PWP_ACT_GELU, v[i]);
       break;
     case PWP_ACT_GELU_TANH:
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = activate(PWP_ACT_GELU_TANH, v[i]);
+      for (int i = 0; i < 32; ++i) v[i] = activate<bf16>(PWP_ACT_GELU_TANH, v[i]);
       break;
     default: break;
   }
@@ -520,8 +520,8 @@ __device__ __forceinline__ void finish_rows(const Skinny& g, const Epilogue& ep,
     }
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      s[0][t] = activate(ACT, s[0][t]);
-      s[1][t] = activate(ACT, s[1][t]);
+      s[0][t] = activate<bf16>(ACT, s[0][t]);
+      s[1][t] = activate<bf16>(ACT, s[1][t]);
       if (GATED) s[0][t] *= s[X - 2][t], s[1][t] *= s[X - 1][t];
     }
     const long long r = row0 + 4 * rg;

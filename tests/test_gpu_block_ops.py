@@ -764,3 +764,38 @@ def test_prune_decoder_block():
                                          block=64)
     s.synchronize()
     assert torch.equal(out2, out) and all(torch.equal(res2[p][0], res[p][0]) for p in w)
+
+
+# ------------------------------------------------------------------- activations by themselves
+
+def check_activation(act, dtype, lo, hi, rel, atol, want=None):
+    """Relative to the result, in the tails too; few rows and many, alone and times an up product of
+    2^20, which lifts a small result over what an absolute bound would forgive.  x has the values
+    and a column of ones, the weights pick one: both products are exact, and so are the sums."""
+    torch, pwp = _torch(), _pwp()
+    pick = lambda k, v: torch.zeros(40, 8, device="cuda").index_fill_(1, torch.tensor([k], device="cuda"), v).to(dt(dtype))
+    for count, repeat in ((97, 1), (3001, 2)):
+        x = torch.zeros(count * repeat, 8, dtype=dt(dtype), device="cuda")
+        x[:, 0] = torch.linspace(lo, hi, count, dtype=torch.float64).to(dt(dtype)).cuda().repeat(repeat)
+        x[:, 1] = 1.0
+        t = np64(x[:, :1])
+        y = F.activation(act, t) if want is None else want(t)
+        tol = (np.abs(y) * (rel(t) + U(x.dtype)) + atol(t)) * np.ones((1, 40))
+        y = y * np.ones((1, 40))
+        close(pwp.linear(x, pick(0, 1.0), activation=act), y, tol, act)
+        got = pwp.gated_linear(x, pick(0, 1.0), pick(1, 2.0 ** 20), activation=act)
+        close(got, y * 2.0 ** 20, tol * 2.0 ** 20, "gated " + act)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lo,hi", [(-8.0, -3.0), (-12.9, -8.0), (-3.0, 3.0), (3.0, 20.0)])
+def test_gelu_in_the_tails(lo, hi, dtype):
+    """x Phi(x) relative to itself (c = 2^-24, half a step).  fp32, by erfc(t), t = -x / sqrt 2: t is off by
+    c (its rounding) and c / 2 (the constant's), and d ln erfc(t) = -2 t^2 (1 + 1 / (2 t^2)) dt / t at
+    most for t > 0.5, so by (x^2 + 2) 1.5 c; erfc to 4 steps (its documented bound), two products.
+    bf16, by e^(-x^2/2) and a polynomial good to 2^-20: the exponential to 2 + 1.173 x^2 / 2 steps (its
+    documented bound), its argument's rounding x^2 / 2 c, ten more operations of a step each.
+    Below the least normal number (2^-126) results have fewer bits."""
+    rel = (lambda t: (1.5 * (t * t + 2) + 10) * 2.0 ** -24) if dtype == "fp32" else \
+        (lambda t: 2.0 ** -20 + (12 + 0.8365 * t * t) * G)
+    check_activation("gelu", dtype, lo, hi, rel, lambda t: np.abs(t) * 2.0 ** -148)
