@@ -34,8 +34,18 @@ __device__ __forceinline__ float normal_tail(float a) {
   return p * t * __expf(-0.5f * a * a);
 }
 
-// Activations of pwp_activation in fp32, for results of type T.  For x far below zero e^-x
-// overflows to infinity and x / inf is -0, the limit of x / (1 + e^-x).
+// x / (1 + e^-z), z of the sign of x.  e^-|z| never overflows, so results far below zero keep
+// their value down to the smallest numbers (e^-z is infinite from z = -88.7 on, where
+// x e^z is still a normal number).  bf16 takes the fast exponential (off by 2 + 1.17 |z| steps
+// of 2^-23, a hundredth of bf16's half step at |z| = 88) and division (the divisor lies in [1, 2]).
+template <typename T>
+__device__ __forceinline__ float times_logistic(float x, float z) {
+  const float e = sizeof(T) == 4 ? expf(-fabsf(z)) : __expf(-fabsf(z));
+  const float num = z < 0.f ? x * e : x;
+  return sizeof(T) == 4 ? num / (1.f + e) : __fdividef(num, 1.f + e);
+}
+
+// Activations of pwp_activation in fp32, for results of type T.
 //
 // erf-GELU: 1 + erf(x / sqrt 2) would cancel below zero (nothing is left from x = -5.8 on), so
 // fp32 takes erfc, and bf16, whose half step is 2^-8, normal_tail: 16384 x 128 x 8192, where the epilogue
@@ -44,14 +54,14 @@ template <typename T>
 __device__ __forceinline__ float activate(int act, float x) {
   switch (act) {
     case PWP_ACT_RELU: return x != x ? x : fmaxf(x, 0.f);
-    case PWP_ACT_SILU: return __fdividef(x, 1.f + __expf(-x));
+    case PWP_ACT_SILU: return times_logistic<T>(x, x);
     case PWP_ACT_GELU: {
       if (sizeof(T) == 4) return 0.5f * x * erfcf(x * -0.70710678118654752f);
       const float q = normal_tail(fabsf(x));
       return x * (x < 0.f ? q : 1.f - q);
     }
     case PWP_ACT_GELU_TANH:      // (1 + tanh t) / 2 = 1 / (1 + e^-2t)
-      return __fdividef(x, 1.f + __expf(-1.5957691216057308f * (x + 0.044715f * x * x * x)));
+      return times_logistic<T>(x, 1.5957691216057308f * (x + 0.044715f * x * x * x));
     default: return x;
   }
 }

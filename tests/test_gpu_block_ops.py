@@ -771,7 +771,9 @@ def test_prune_decoder_block():
 def check_activation(act, dtype, lo, hi, rel, atol, want=None):
     """Relative to the result, in the tails too; few rows and many, alone and times an up product of
     2^20, which lifts a small result over what an absolute bound would forgive.  x has the values
-    and a column of ones, the weights pick one: both products are exact, and so are the sums."""
+    and a column of ones, the weights pick one: both products are exact, and so are the sums.
+    Below the least normal number, 2^-126, the steps of a type stay those at 2^-126 (bf16: 2^-133),
+    so a result is rounded by up to u 2^-126 (half of that) there."""
     torch, pwp = _torch(), _pwp()
     pick = lambda k, v: torch.zeros(40, 8, device="cuda").index_fill_(1, torch.tensor([k], device="cuda"), v).to(dt(dtype))
     for count, repeat in ((97, 1), (3001, 2)):
@@ -782,9 +784,10 @@ def check_activation(act, dtype, lo, hi, rel, atol, want=None):
         y = F.activation(act, t) if want is None else want(t)
         tol = (np.abs(y) * (rel(t) + U(x.dtype)) + atol(t)) * np.ones((1, 40))
         y = y * np.ones((1, 40))
-        close(pwp.linear(x, pick(0, 1.0), activation=act), y, tol, act)
+        least = U(x.dtype) * 2.0 ** -126
+        close(pwp.linear(x, pick(0, 1.0), activation=act), y, tol + least, act)
         got = pwp.gated_linear(x, pick(0, 1.0), pick(1, 2.0 ** 20), activation=act)
-        close(got, y * 2.0 ** 20, tol * 2.0 ** 20, "gated " + act)
+        close(got, y * 2.0 ** 20, tol * 2.0 ** 20 + least, "gated " + act)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -799,3 +802,42 @@ def test_gelu_in_the_tails(lo, hi, dtype):
     rel = (lambda t: (1.5 * (t * t + 2) + 10) * 2.0 ** -24) if dtype == "fp32" else \
         (lambda t: 2.0 ** -20 + (12 + 0.8365 * t * t) * G)
     check_activation("gelu", dtype, lo, hi, rel, lambda t: np.abs(t) * 2.0 ** -148)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("act,lo,hi", [("silu", -20.0, 20.0), ("silu", -91.0, -20.0), ("gelu_tanh", -5.0, 5.0),
+                                       ("gelu_tanh", -10.5, -5.0), ("gelu_tanh", 5.0, 200.0)])
+def test_logistic_activations_in_the_tails(act, lo, hi, dtype):
+    """x / (1 + e^-z) relative to itself, z = x (SiLU) or 2 sqrt(2/pi) (x + 0.044715 x^3), which is off by 6
+    half steps (four operations, two constants): |z| 6 2^-24 of the result.  fp32: the exponential to 2
+    steps (documented: 1), the sum, product and quotient to half a step each.  bf16: the exponential
+    to 2 + 1.173 |z| steps and the quotient to 2 (documented).  Exponentials below the least normal
+    number (2^-126) are off by 2^-149."""
+    def z(t):
+        return t if act == "silu" else 2 * math.sqrt(2 / math.pi) * (t + 0.044715 * t ** 3)
+
+    def want(t):           # no sum that cancels
+        e = np.exp(-np.abs(z(t)))
+        return np.where(z(t) < 0, t * e, t) / (1 + e)
+    arg = (lambda t: 0 * t) if act == "silu" else (lambda t: 6 * 2.0 ** -24 * np.minimum(np.abs(z(t)), 90.0))
+    rel = (lambda t: arg(t) + 4 * G) if dtype == "fp32" else \
+        (lambda t: arg(t) + (7 + 1.173 * np.minimum(np.abs(z(t)), 90.0)) * G)
+    check_activation(act, dtype, lo, hi, rel, lambda t: np.abs(t) * 2.0 ** -148, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_activations_of_special_values(dtype):
+    """What the formulas give: +inf stays, NaN stays, and at -inf only ReLU has a limit the formula takes."""
+    torch, pwp = _torch(), _pwp()
+    for rows in (4, 3000):
+        x = torch.zeros(rows, 8, dtype=dt(dtype), device="cuda")
+        x[:4, 0] = torch.tensor([math.inf, -math.inf, math.nan, -3e38], dtype=dt(dtype))
+        w = torch.zeros(40, 8, dtype=dt(dtype), device="cuda")
+        w[:, 0] = 1.0
+        for act in ACTS:
+            y = pwp.linear(x, w, activation=act)
+            assert bool((y[0] == math.inf).all()) and bool(y[2].isnan().all()), act
+            assert act == "none" or bool((y[3] == 0).all()), act
+            assert not bool(y[4:].any())
+            if act == "relu":
+                assert bool((y[1] == 0).all())
