@@ -841,3 +841,24 @@ def test_activations_of_special_values(dtype):
             assert not bool(y[4:].any())
             if act == "relu":
                 assert bool((y[1] == 0).all())
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("d", [128, 36])                # registers, and (36 turned of 38) shared memory
+def test_rotation_angles_in_fp32(d, layout):
+    """Cosines and sines by themselves (q = (1, 0) in every pair), relative to each: sincospif to 2 steps
+    (documented: 1 for the sine, 1 for the cosine), the turn by the angle's rest to one rounding, half a
+    step.  Near a zero the turn is all there is: at most 2^-23.3, its rest rounded twice and times a
+    sine off by two steps (six half steps, 2^-44.7) and its second term (2^-47): 2^-44.  The reduced
+    angle's 64-bit error is 4 2^-53 of position * f radians (three roundings, and 1 / 2 pi's)."""
+    torch, pwp = _torch(), _pwp()
+    n, width = 4000, d + (d == 36) * 2
+    pos = torch.arange(n, device="cuda")
+    f, _ = pwp.rope_frequencies(d, base=500.0)
+    q = torch.zeros(n, 1, width, device="cuda")
+    one, other = (slice(0, d // 2), slice(d // 2, d)) if layout == "half" else (slice(0, d, 2), slice(1, d, 2))
+    q[..., one] = 1.0
+    y = pwp.qk_norm_rope(q, q[:, :0], pos, f, layout=layout)[0]
+    angle = np.arange(n)[:, None] * np64(f)[None]
+    for got, want in ((y[:, 0, one], np.cos(angle)), (y[:, 0, other], np.sin(angle))):
+        close(got, want, np.abs(want) * 2.5 * G + 4 * 2.0 ** -53 * angle + 2.0 ** -44)
