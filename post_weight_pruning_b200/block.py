@@ -10,7 +10,8 @@ with those inputs and passes the hidden states through the pruned layers.
 
 The operators run on the device of their tensors and on the given or the current stream of
 that device; nothing synchronises and nothing is kept between calls.  They compute a forward
-pass only: an input that requires a gradient is refused while gradients are recorded.
+pass only: an input that requires a gradient is refused while gradients are recorded, and
+one that carries a forward-mode tangent always.
 """
 from __future__ import annotations
 
@@ -183,11 +184,14 @@ def _check_out(t, name, shape, like, others, same=None):
 
 
 def _forward_only(*ts):
-    if _torch().is_grad_enabled():
-        for t in ts:
-            if t is not None and t.requires_grad:
-                raise ValueError("the operators compute a forward pass only: call them under torch.no_grad() "
-                                 "or on detached tensors")
+    torch = _torch()
+    recording, forward = torch.is_grad_enabled(), torch.autograd.forward_ad
+    dual = forward._current_level >= 0
+    for t in ts:
+        if t is not None and ((recording and t.requires_grad) or
+                              (dual and forward.unpack_dual(t).tangent is not None)):
+            raise ValueError("the operators compute a forward pass only: call them under torch.no_grad() "
+                             "or on detached tensors, without forward-mode tangents")
 
 
 def _ptr(t):

@@ -33,7 +33,7 @@ struct Call {
     const at::Tensor& t = THPVariable_Unpack(o);
     if (!t.defined() || !t.is_cuda() || !t.has_storage() || t.layout() != at::kStrided || t.is_neg() || t.dim() != dims ||
         t.get_device() != device || t.scalar_type() != want || (recording && t.requires_grad()) ||
-        t._is_zerotensor())
+        t._fw_grad(/*level=*/0).defined() || t._is_zerotensor())
       return nullptr;
     return t.size(-1) > 1 && t.stride(-1) != 1 ? nullptr : &t;
   }

@@ -480,3 +480,25 @@ def test_queries_given_as_keys_too(fake):
     pwp.qk_norm_rope(q, q, POS4, FR, q_out=z(4, 3, 8))
     pwp.linear(SQ, z(8, 8), residual=SQ)
     assert len(fake.calls) == 3
+
+
+# ------------------------------------------------------------------- derivatives
+
+def test_forward_mode_tangents_are_refused(fake):
+    import torch.autograd.forward_ad as fwd
+    with fwd.dual_level():
+        dual = lambda *shape: fwd.make_dual(z(*shape), z(*shape))
+        for recording in (True, False):
+            with torch.set_grad_enabled(recording):
+                for call in (lambda: pwp.rms_norm(dual(2, 4)), lambda: pwp.rms_norm(z(2, 4), dual(4)),
+                             lambda: pwp.rms_norm(z(2, 4), out=dual(2, 4)),
+                             lambda: pwp.qk_norm_rope(z(2, 3, 4), dual(2, 3, 4), POS, FR),
+                             lambda: pwp.attention(z(2, 2, 4), z(2, 2, 4), dual(2, 2, 4), CU),
+                             lambda: pwp.linear(z(2, 4), dual(3, 4)), lambda: pwp.linear(z(2, 4), z(3, 4), residual=dual(2, 3)),
+                             lambda: pwp.gated_linear(z(2, 4), z(3, 4), dual(3, 4))):
+                    with pytest.raises(ValueError, match="forward pass"):
+                        call()
+        assert not fake.calls
+        pwp.rms_norm(z(2, 4))                # a level alone, and what a dual was made of, are no matter
+        pwp.rms_norm(fwd.unpack_dual(dual(2, 4)).primal)
+    assert len(fake.calls) == 2

@@ -862,3 +862,19 @@ def test_rotation_angles_in_fp32(d, layout):
     angle = np.arange(n)[:, None] * np64(f)[None]
     for got, want in ((y[:, 0, one], np.cos(angle)), (y[:, 0, other], np.sin(angle))):
         close(got, want, np.abs(want) * 2.5 * G + 4 * 2.0 ** -53 * angle + 2.0 ** -44)
+
+
+def test_forward_mode_tangents_are_refused():
+    """Also by the usual calls, which the C++ marshalling takes otherwise."""
+    torch, pwp = _torch(), _pwp()
+    import torch.autograd.forward_ad as fwd
+    x, w = rnd((4, 64), "bf16", 171), rnd((16, 64), "bf16", 172)
+    q, pos, (f, _) = rnd((4, 2, 64), "bf16", 173), torch.arange(4, device="cuda"), pwp.rope_frequencies(64)
+    cu = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    with fwd.dual_level():
+        dual = lambda t: fwd.make_dual(t, torch.ones_like(t))
+        for call in (lambda g: pwp.rms_norm(g(x)), lambda g: pwp.linear(x, g(w)), lambda g: pwp.gated_linear(g(x), w, w),
+                     lambda g: pwp.attention(q, q, g(q), cu), lambda g: pwp.qk_norm_rope(g(q), q, pos, f)):
+            with torch.no_grad(), pytest.raises(ValueError, match="forward pass"):
+                call(dual)
+            call(lambda t: t)
