@@ -342,7 +342,7 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
         _check_tensor(q_weight, "q_weight", (d,), q)
     if k_weight is not None:
         _check_tensor(k_weight, "k_weight", (d,), q)
-    _forward_only(q, k, q_weight, k_weight)
+    _forward_only(q, k, freqs, q_weight, k_weight)
     if q_out is None:
         q_out = q.new_empty(q_shape)
     else:

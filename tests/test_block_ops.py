@@ -502,3 +502,12 @@ def test_forward_mode_tangents_are_refused(fake):
         pwp.rms_norm(z(2, 4))                # a level alone, and what a dual was made of, are no matter
         pwp.rms_norm(fwd.unpack_dual(dual(2, 4)).primal)
     assert len(fake.calls) == 2
+
+
+def test_frequencies_that_require_a_gradient_are_refused(fake):
+    with pytest.raises(ValueError, match="forward pass"):
+        pwp.qk_norm_rope(z(2, 3, 4), z(2, 3, 4), POS, FR.clone().requires_grad_())
+    import torch.autograd.forward_ad as fwd
+    with fwd.dual_level(), pytest.raises(ValueError, match="forward pass"):
+        pwp.qk_norm_rope(z(2, 3, 4), z(2, 3, 4), POS, fwd.make_dual(FR, FR))
+    assert not fake.calls
