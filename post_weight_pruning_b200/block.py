@@ -259,19 +259,26 @@ def rope_frequencies(rot, *, base=10000.0, scaling=None, device="cuda"):
       {"type": "yarn", "factor": s, "original_max_positions": n0, "beta_fast": 32.0,
        "beta_slow": 1.0}                     the same idea with the ramp linear in the pair's
                                              index, between the pairs that make beta_fast and
-                                             beta_slow turns; factor 0.1 ln s + 1"""
+                                             beta_slow turns; factor 0.1 ln s + 1 (1 for s up to 1)"""
     torch = _torch()
     rot = int(rot)
-    if rot < 0 or rot % 2 or not base > 0:
+    if rot < 0 or rot % 2 or not 0 < base < math.inf:
         raise ValueError(f"rot even and base > 0 expected, got {rot} and {base}")
     i = np.arange(0, rot, 2, dtype=np.float64)
     f = float(base) ** (-i / max(rot, 1))
     factor = 1.0
     if scaling is not None:
         sc = dict(scaling)
-        kind, s = sc.pop("type", None), float(sc.pop("factor", 0.0))
-        if not s > 0:
-            raise ValueError(f"scaling: factor > 0 expected, got {scaling}")
+        kind = sc.pop("type", None)
+
+        def entry(name, *default, zero=False):
+            if name not in sc and not default:
+                raise ValueError(f"scaling: {name} missing in {scaling}")
+            x = float(sc.pop(name, *default))
+            if not (0 < x < math.inf or (zero and x == 0)):
+                raise ValueError(f"scaling: {name} {'>=' if zero else '>'} 0 expected, got {x}")
+            return x
+        s = entry("factor")
         if kind == "linear":
             f = f / s
         elif kind == "base":
@@ -279,20 +286,20 @@ def rope_frequencies(rot, *, base=10000.0, scaling=None, device="cuda"):
                 raise ValueError("scaling by the base needs rot > 2")
             f = (float(base) * s ** (rot / (rot - 2))) ** (-i / rot)
         elif kind == "bands":
-            lo, hi = float(sc.pop("low_freq_factor")), float(sc.pop("high_freq_factor"))
-            n0 = float(sc.pop("original_max_positions"))
+            lo, hi, n0 = entry("low_freq_factor", zero=True), entry("high_freq_factor"), entry("original_max_positions")
             if not hi > lo:
                 raise ValueError("scaling: high_freq_factor > low_freq_factor expected")
             keep = np.clip((n0 * f / (2 * math.pi) - lo) / (hi - lo), 0.0, 1.0)
             f = f * (keep + (1.0 - keep) / s)
         elif kind == "yarn":
-            n0 = float(sc.pop("original_max_positions"))
-            fast, slow = float(sc.pop("beta_fast", 32.0)), float(sc.pop("beta_slow", 1.0))
+            n0, fast, slow = entry("original_max_positions"), entry("beta_fast", 32.0), entry("beta_slow", 1.0)
+            if not base > 1:
+                raise ValueError(f"scaling: yarn needs base > 1, got {base}")
             pair = lambda turns: rot * math.log(n0 / (turns * 2 * math.pi)) / (2 * math.log(base))
             lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rot - 1)
             slowed = np.clip((np.arange(rot // 2) - lo) / max(hi - lo, 1e-3), 0.0, 1.0)
             f = f * (1.0 - slowed) + f / s * slowed
-            factor = 0.1 * math.log(s) + 1.0
+            factor = 0.1 * math.log(s) + 1.0 if s > 1 else 1.0
         else:
             raise ValueError(f"scaling: unknown type {kind!r}")
         if sc:

@@ -511,3 +511,58 @@ def test_frequencies_that_require_a_gradient_are_refused(fake):
     with fwd.dual_level(), pytest.raises(ValueError, match="forward pass"):
         pwp.qk_norm_rope(z(2, 3, 4), z(2, 3, 4), POS, fwd.make_dual(FR, FR))
     assert not fake.calls
+
+
+# ------------------------------------------------------------------- frequencies between the ends
+
+def test_yarn_leaves_short_contexts_their_factor():
+    for s in (0.5, 1.0):
+        sc = dict(type="yarn", factor=s, original_max_positions=4096)
+        assert pwp.rope_frequencies(64, scaling=sc, device="cpu")[1] == 1.0
+    sc["factor"] = 1.5
+    assert math.isclose(pwp.rope_frequencies(64, scaling=sc, device="cpu")[1], 0.1 * math.log(1.5) + 1, rel_tol=1e-15)
+
+
+def test_scaled_frequencies_on_the_ramp():
+    rot, base, s, n0 = 64, 500.0, 8.0, 2000
+    plain = [base ** (-2 * i / rot) for i in range(rot // 2)]
+    sc = dict(type="bands", factor=s, low_freq_factor=1.0, high_freq_factor=5.0, original_max_positions=n0)
+    f, between = pwp.rope_frequencies(rot, base=base, scaling=sc, device="cpu")[0], 0
+    for i, p in enumerate(plain):
+        turns = n0 * p / (2 * math.pi)
+        t = min(max((turns - 1.0) / 4.0, 0.0), 1.0)
+        between += 0 < t < 1
+        assert math.isclose(float(f[i]), t * p + (1 - t) * p / s, rel_tol=1e-13), i
+    assert between >= 3
+    sc["low_freq_factor"] = 0                  # a ramp from the slowest pairs on
+    f = pwp.rope_frequencies(rot, base=base, scaling=sc, device="cpu")[0]
+    t = min(n0 * plain[-1] / (2 * math.pi) / 5.0, 1.0)
+    assert math.isclose(float(f[-1]), t * plain[-1] + (1 - t) * plain[-1] / s, rel_tol=1e-13)
+    # pairs that make 32 turns and 1 turn over the positions, rounded outwards
+    sc = dict(type="yarn", factor=s, original_max_positions=n0)
+    place = lambda turns: rot / 2 * math.log(n0 / (2 * math.pi * turns)) / math.log(base)
+    lo, hi = math.floor(place(32.0)), math.ceil(place(1.0))
+    assert 0 < lo < hi - 3 and hi < rot // 2
+    f = pwp.rope_frequencies(rot, base=base, scaling=sc, device="cpu")[0]
+    for i, p in enumerate(plain):
+        t = min(max((i - lo) / (hi - lo), 0.0), 1.0)
+        assert math.isclose(float(f[i]), (1 - t) * p + t * p / s, rel_tol=1e-13), i
+
+
+@pytest.mark.parametrize("sc", [
+    dict(type="yarn", factor=2), dict(type="yarn", factor=2, original_max_positions=-5),
+    dict(type="yarn", factor=2, original_max_positions=0), dict(type="yarn", factor=2, original_max_positions=9, beta_fast=0),
+    dict(type="yarn", factor=2, original_max_positions=9, beta_slow=-1), dict(type="yarn", factor=math.inf, original_max_positions=9),
+    dict(type="bands", factor=2, low_freq_factor=1, high_freq_factor=4),
+    dict(type="bands", factor=2, low_freq_factor=1, original_max_positions=10),
+    dict(type="bands", factor=2, low_freq_factor=1, high_freq_factor=4, original_max_positions=-10),
+    dict(type="linear", factor=math.nan), dict(type="linear", factor=math.inf)])
+def test_scalings_without_their_entries_are_refused(sc):
+    with pytest.raises(ValueError, match="scaling"):
+        pwp.rope_frequencies(16, scaling=sc, device="cpu")
+
+
+def test_bases_out_of_range_are_refused():
+    for kw in (dict(base=math.inf), dict(base=math.nan), dict(base=1.0, scaling=dict(type="yarn", factor=2, original_max_positions=9))):
+        with pytest.raises(ValueError, match="base"):
+            pwp.rope_frequencies(16, **kw, device="cpu")
