@@ -687,6 +687,7 @@ __global__ void __launch_bounds__(kThreadsAtt, 1)
           __syncwarp();
         }
       }
+      __syncwarp();      // every lane has read the item, also of a tile without rows
       if (lane == 0) mbar_arrive(&sb.iempty[iq.slot]);
       iq.step();
       ++item;

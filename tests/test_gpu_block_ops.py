@@ -878,3 +878,19 @@ def test_forward_mode_tangents_are_refused():
             with torch.no_grad(), pytest.raises(ValueError, match="forward pass"):
                 call(dual)
             call(lambda t: t)
+
+
+@pytest.mark.parametrize("hq,hk,per", [(2, 2, 128), (8, 2, 32)])
+def test_attention_many_items_whose_second_tile_is_empty(hq, hk, per):
+    """Sequences of at most one tile of queries (`per` tokens): every item's second tile has no rows, and its
+    softmax warps release one item after another without work of their own."""
+    pwp = _pwp()
+    rng = np.random.default_rng(181)
+    lens = rng.integers(1, per + 1, size=900).tolist()
+    q, k, v, cu = att_case(lens, hq, hk, 64, "bf16", 182)
+    want, size = F.attention(np64(q), np64(k), np64(v), lens, True, spread=True)
+    tol = att_tol(q, k, lens, hq, hk, 64, want, size, "bf16")
+    for _ in range(3):
+        st = pwp.new_stats()
+        close(pwp.attention(q, k, v, cu, stats=st), want, tol)
+        assert pwp.read_stats(st).status == 0
