@@ -117,16 +117,21 @@ __device__ __forceinline__ void remote_store(uint32_t addr, float v) {
 struct SeqTile {
   int begin, len, first;
 };
+// Where a search stands: the first sequence of its chunk of 32, and the tiles before it.
+struct SeqScan {
+  int s0 = 0, base = 0;
+};
 
 // Finds tile `t` when every sequence is cut into tiles of `per` rows (whole warp, all lanes
-// get the answer).  The first sequence whose offsets decrease or leave [0, n] and all behind
-// it count as empty, so the sequences taken never overlap; `bad` is set when one is met.
-// Returns false past the last tile.
+// get the answer).  `scan` goes on from call to call: t never decreases, and a CTA that takes many
+// tiles reads the offsets once, however many sequences there are.  The first sequence whose
+// offsets decrease or leave [0, n] and all behind it count as empty, so the sequences taken
+// never overlap; `bad` is set when one is met.  Returns false past the last tile.
 __device__ __forceinline__ bool find_seq_tile(const int* __restrict__ cu, int nseq, long long n, int per, int t,
-                                              SeqTile& out, bool& bad) {
+                                              SeqScan& scan, SeqTile& out, bool& bad) {
   const int lane = threadIdx.x & 31;
-  for (int s0 = 0; s0 < nseq; s0 += 32) {
-    const int s = s0 + lane;
+  for (; scan.s0 < nseq; scan.s0 += 32) {
+    const int s = scan.s0 + lane;
     int a = 0, b = 0;
     if (s < nseq) {
       a = cu[s];
@@ -143,16 +148,19 @@ __device__ __forceinline__ bool find_seq_tile(const int* __restrict__ cu, int ns
       const int v = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += v;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, t < sum);
+    const unsigned hit = __ballot_sync(0xffffffffu, t < scan.base + sum);
     if (hit) {
       const int l = __ffs(hit) - 1;
       out.begin = __shfl_sync(0xffffffffu, a, l);
       out.len = __shfl_sync(0xffffffffu, len, l);
-      out.first = (t - __shfl_sync(0xffffffffu, sum - tiles, l)) * per;
+      out.first = (t - scan.base - __shfl_sync(0xffffffffu, sum - tiles, l)) * per;
       return true;
     }
-    if (broken) return false;
-    t -= __shfl_sync(0xffffffffu, sum, 31);
+    if (broken) {
+      scan.s0 = nseq;
+      return false;
+    }
+    scan.base += __shfl_sync(0xffffffffu, sum, 31);
   }
   return false;
 }

@@ -894,3 +894,53 @@ def test_attention_many_items_whose_second_tile_is_empty(hq, hk, per):
         st = pwp.new_stats()
         close(pwp.attention(q, k, v, cu, stats=st), want, tol)
         assert pwp.read_stats(st).status == 0
+
+
+@pytest.mark.parametrize("dtype,d", [("fp32", 33), ("bf16", 64)])
+def test_attention_of_a_few_tokens_among_very_many_sequences(dtype, d):
+    """A million offsets, nearly all of empty sequences: the offsets are read a bounded number of times."""
+    torch, pwp = _torch(), _pwp()
+    nseq, hq, n = 1 << 20, 4, 150
+    lens = np.zeros(nseq, dtype=np.int64)
+    at = np.random.default_rng(191).choice(nseq, size=50, replace=False)
+    lens[at] = 3
+    assert lens.sum() == n
+    q, k, v, cu = att_case(lens.tolist(), hq, 2, d, dtype, 192)
+    few = [3] * 50
+    want, size = F.attention(np64(q), np64(k), np64(v), few, True, spread=True)
+    st = pwp.new_stats()
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    got = pwp.attention(q, k, v, cu, stats=st)
+    b.record()
+    torch.cuda.synchronize()
+    assert pwp.read_stats(st).status == 0
+    close(got, want, att_tol(q, k, few, hq, 2, d, want, size, dtype))
+    assert a.elapsed_time(b) < 2000.0
+    cu[-1] = n + 1                                        # the last sequence leaves the batch
+    out = torch.full_like(q, 7.0)
+    pwp.attention(q, k, v, cu, out=out, stats=st)
+    assert pwp.read_stats(st).status == 1
+    first = int(cu[-2])
+    assert torch.equal(out[:first], got[:first]) and bool((out[first:] == 7.0).all())
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_on_the_cuda_cores_several_tiles_a_cta(causal):
+    """More tiles than CTAs: each takes several, of several sequences and heads, in one go."""
+    torch, pwp = _torch(), _pwp()
+    lens = [300, 0, 64, 1, 65, 130] * 12
+    n, hq = sum(lens), 24
+    q, k, v, cu = att_case(lens, hq, 2, 20, "fp32", 193, extra=3)
+    out = torch.full_like(q, 7.0)
+    pwp.attention(q, k, v, cu, causal=causal, out=out)
+    assert bool((out[n:] == 7.0).all())
+    at = 0
+    for length in lens:
+        s = slice(at, at + length)
+        if length:
+            alone = pwp.attention(q[s], k[s], v[s], torch.tensor([0, length], dtype=torch.int32, device="cuda"), causal=causal)
+            assert torch.equal(alone, out[s])
+        at += length
+    want, size = F.attention(np64(q[430:560]), np64(k[430:560]), np64(v[430:560]), [130], causal, spread=True)
+    close(out[430:560], want, att_tol(q, k, lens, hq, 2, 20, want, size, "fp32"))
