@@ -3,8 +3,9 @@
     python -m post_weight_pruning_b200.build          # or build() from Python
 
 Objects go to _build/ at the repository root; the shared library is written next
-to this file so the Python binding finds it.  Where PyTorch is installed, _fastcall.so (the
-forward operators' usual calls, marshalled without the interpreter) is built beside it.
+to this file so the Python binding finds it.  Where PyTorch for CUDA and g++ are installed, _fastcall
+(the forward operators' usual calls, marshalled without the interpreter) is built beside it;
+where it cannot be, a warning says so and the binding marshals those calls itself.
 """
 from __future__ import annotations
 
@@ -16,13 +17,15 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(ROOT, "_build", "obj")
 LIB = os.path.join(HERE, "libpwp.so")
-FASTCALL = os.path.join(HERE, "_fastcall.so")
+# named for this interpreter: another one does not import it
+FASTCALL = os.path.join(HERE, "_fastcall" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + os.path.join(ROOT, "include")]
@@ -51,27 +54,54 @@ def _compile(src, extra, verbose):
     return obj
 
 
+def _read(path):
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
+def _remove(path):
+    if os.path.exists(path):
+        os.remove(path)
+
+
 def _build_fastcall(verbose):
-    """g++ against PyTorch's headers and libpwp.so, which is found beside it at run time."""
+    """g++ against PyTorch's headers and libpwp.so, which is found beside it at run time.  Built
+    again when its sources, the command or PyTorch's version are others than those recorded
+    with the objects."""
+    _remove(os.path.join(HERE, "_fastcall.so"))      # a build without the interpreter's tag
     spec = importlib.util.find_spec("torch")
     if spec is None:
         return
     torch = os.path.dirname(spec.origin)
     src = os.path.join(CSRC, "fastcall.cpp")
     header = os.path.join(ROOT, "include", "pwp.h")
-    if os.path.exists(FASTCALL) and os.path.getmtime(FASTCALL) >= max(os.path.getmtime(src), os.path.getmtime(header)):
-        return
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
     lib = os.path.join(torch, "lib")
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", src, "-o", FASTCALL, *("-I" + p for p in inc), "-L" + HERE,
            "-l:libpwp.so", "-Wl,-rpath,$ORIGIN", "-L" + lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
+    record, built_for = os.path.join(OBJ, "fastcall.txt"), " ".join(cmd) + "\n" + (_read(os.path.join(torch, "version.py")) or "")
+    if os.path.exists(FASTCALL) and _read(record) == built_for and \
+            os.path.getmtime(FASTCALL) >= max(os.path.getmtime(src), os.path.getmtime(header)):
+        return
+    _remove(FASTCALL)          # what does not fit this PyTorch or pwp.h is not left to be loaded
     if verbose:
         print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        failed = f"{r.stdout}\n{r.stderr}" if r.returncode != 0 else None
+    except OSError as e:
+        failed = str(e)
+    if failed is not None:
+        _remove(FASTCALL)
+        warnings.warn(f"{os.path.basename(FASTCALL)} not built, small calls of the forward operators take longer:\n{failed}")
+        return
+    with open(record, "w") as f:
+        f.write(built_for)
 
 
 def build(verbose: bool = False, extra=()) -> str:
