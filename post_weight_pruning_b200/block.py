@@ -582,6 +582,7 @@ def prune_decoder_block(weights, hidden, seq_lens, *, forward, stream=None, **cf
     weights = {name: weights[name] for name in FEEDS if name in weights}
     acts, _ = block_forward(weights, hidden, seq_lens, stream=stream, **forward)
     results = _pwp.prune_block(weights, acts, FEEDS, stream=stream, **cfg)
+    del acts      # the second pass allocates its own
     if stream is None:
         pruned = {name: results[name][0].to(weights[name].dtype) for name in FEEDS}
     else:

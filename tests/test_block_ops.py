@@ -566,3 +566,19 @@ def test_bases_out_of_range_are_refused():
     for kw in (dict(base=math.inf), dict(base=math.nan), dict(base=1.0, scaling=dict(type="yarn", factor=2, original_max_positions=9))):
         with pytest.raises(ValueError, match="base"):
             pwp.rope_frequencies(16, **kw, device="cpu")
+
+
+def test_the_dense_activations_are_free_before_the_second_pass(monkeypatch):
+    import weakref
+    alive = []
+
+    def block_forward(weights, hidden, seq_lens, **kw):
+        alive.append(sum(r() is not None for r in refs))
+        acts = {name: z(4, 8) for name in set(B.FEEDS.values())}
+        refs.extend(weakref.ref(t) for t in acts.values())
+        return acts, hidden
+    refs = []
+    monkeypatch.setattr(B, "block_forward", block_forward)
+    monkeypatch.setattr(pwp, "prune_block", lambda weights, acts, feeds, **kw: {p: (w, None, None) for p, w in weights.items()})
+    results, out = pwp.prune_decoder_block({p: z(8, 8) for p in B.FEEDS}, z(4, 8), [4], forward={})
+    assert set(results) == set(B.FEEDS) and alive == [0, 0]
