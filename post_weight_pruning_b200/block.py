@@ -538,8 +538,8 @@ def block_forward(weights, hidden, seq_lens, *, heads, kv_heads=None, freqs=None
     if heads < 1 or kv_heads < 1 or heads % kv_heads or weights["q_proj"].shape[0] % heads:
         raise ValueError(f"{heads} query heads, {kv_heads} key heads, q_proj {tuple(weights['q_proj'].shape)}")
     d = weights["q_proj"].shape[0] // heads
-    if stream is not None:
-        with torch.cuda.device(hidden.device), _pwp._stream_ctx(stream):
+    if _away(hidden, stream):
+        with _at(hidden, stream):
             return block_forward(weights, hidden, lens, heads=heads, kv_heads=kv_heads, freqs=freqs, factor=factor,
                                  layout=layout, positions=positions, norms=norms, biases=biases,
                                  activation=activation, eps=eps, causal=causal, scale=scale, stats=stats)
@@ -579,14 +579,13 @@ def prune_decoder_block(weights, hidden, seq_lens, *, forward, stream=None, **cf
     ``prune_layer`` (method, pattern, sparsity, ...).  Returns (results, out): {layer: (W_hat
     fp32, mask, Stats)} and the pruned block's output, the next block's hidden states.  The
     pruned weights take part in that pass rounded to the weights' type."""
+    if _away(hidden, stream):
+        with _at(hidden, stream):
+            return prune_decoder_block(weights, hidden, seq_lens, forward=forward, **cfg)
     weights = {name: weights[name] for name in FEEDS if name in weights}
-    acts, _ = block_forward(weights, hidden, seq_lens, stream=stream, **forward)
-    results = _pwp.prune_block(weights, acts, FEEDS, stream=stream, **cfg)
+    acts, _ = block_forward(weights, hidden, seq_lens, **forward)
+    results = _pwp.prune_block(weights, acts, FEEDS, **cfg)
     del acts      # the second pass allocates its own
-    if stream is None:
-        pruned = {name: results[name][0].to(weights[name].dtype) for name in FEEDS}
-    else:
-        with _pwp._stream_ctx(stream):
-            pruned = {name: results[name][0].to(weights[name].dtype) for name in FEEDS}
-    _, out = block_forward(pruned, hidden, seq_lens, stream=stream, **forward)
+    pruned = {name: results[name][0].to(weights[name].dtype) for name in FEEDS}
+    _, out = block_forward(pruned, hidden, seq_lens, **forward)
     return results, out

@@ -582,3 +582,45 @@ def test_the_dense_activations_are_free_before_the_second_pass(monkeypatch):
     monkeypatch.setattr(pwp, "prune_block", lambda weights, acts, feeds, **kw: {p: (w, None, None) for p, w in weights.items()})
     results, out = pwp.prune_decoder_block({p: z(8, 8) for p in B.FEEDS}, z(4, 8), [4], forward={})
     assert set(results) == set(B.FEEDS) and alive == [0, 0]
+
+
+BLOCK_W = {p: z(8, 8) for p in B.FEEDS}
+BLOCK_CALLS = [lambda **kw: pwp.block_forward(BLOCK_W, z(4, 8), [4], heads=1, **kw),
+               lambda **kw: pwp.prune_decoder_block(BLOCK_W, z(4, 8), [4], forward=dict(heads=1), **kw)]
+
+
+@pytest.mark.parametrize("call", BLOCK_CALLS)
+def test_the_block_refuses_a_stream_of_another_device(fake, monkeypatch, call):
+    class Stream:
+        device_index = 1
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    monkeypatch.setattr(pwp, "_stream_ctx", lambda s: pytest.fail("entered"))
+    with pytest.raises(ValueError, match="stream of device 1"):
+        call(stream=Stream())
+    assert not fake.calls
+
+
+@pytest.mark.parametrize("call", BLOCK_CALLS)
+def test_the_block_runs_on_its_tensors_device(fake, monkeypatch, call):
+    """From another current device every kernel, the prune's among them, is launched on the tensors' one."""
+    import contextlib
+    current, seen = [1], []
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    monkeypatch.setattr(B, "_current_device", lambda: current[-1])
+
+    @contextlib.contextmanager
+    def device(d):
+        current.append(0)
+        yield
+        current.pop()
+    monkeypatch.setattr(torch.cuda, "device", device)
+
+    def prune_block(weights, acts, feeds, **kw):
+        seen.append(current[-1])
+        return {p: (w, None, None) for p, w in weights.items()}
+    monkeypatch.setattr(pwp, "prune_block", prune_block)
+    record = B._stream_of
+    monkeypatch.setattr(B, "_stream_of", lambda dev: seen.append(current[-1]) or record(dev))
+    monkeypatch.setattr(B, "_fast", B._NoFastCalls)
+    call()
+    assert len(seen) >= 8 and set(seen) == {0} and current == [1]
