@@ -488,6 +488,8 @@ def gated_linear(x, w_gate, w_up, *, bias_gate=None, bias_up=None, activation="s
     """activation(x w_gate^T + bias_gate) * (x w_up^T + bias_up): both projections of a gated
     feed-forward block, the activation and the product in one kernel.  Shapes, types and the
     other arguments as for ``linear``."""
+    if w_up is None:
+        raise TypeError("w_up: tensor expected, got NoneType (without it: linear)")
     if out is None and stream is None:
         y = (_fast or _fast_calls()).linear(x, w_gate, w_up, bias_gate, bias_up, ACTIVATIONS.get(activation), None, stats)
         if y is not None:

@@ -624,3 +624,10 @@ def test_the_block_runs_on_its_tensors_device(fake, monkeypatch, call):
     monkeypatch.setattr(B, "_fast", B._NoFastCalls)
     call()
     assert len(seen) >= 8 and set(seen) == {0} and current == [1]
+
+
+def test_a_gated_product_needs_both_weights(fake):
+    for kw in (dict(), dict(out=z(2, 3))):
+        with pytest.raises(TypeError, match="w_up"):
+            pwp.gated_linear(z(2, 4), z(3, 4), None, **kw)
+    assert not fake.calls
