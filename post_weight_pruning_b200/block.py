@@ -202,6 +202,8 @@ def _stats_ptr(stats, like):
     if stats is None:
         return 0
     _check_tensor(stats, "stats", (ctypes.sizeof(_pwp.Stats),), like, _torch().uint8)
+    if stats.data_ptr() % 8:
+        raise ValueError("stats: a record at a multiple of 8 bytes expected (new_stats gives one)")
     return stats.data_ptr()
 
 

@@ -8,6 +8,8 @@ namespace {
 
 bool valid_type(int32_t t) { return t == PWP_BF16 || t == PWP_FP32; }
 bool finite_f(float x) { return x - x == 0.f; }
+// the kernels' atomics on a record need its own alignment
+bool valid_stats(const pwp_stats* st) { return ((uintptr_t)st & (alignof(pwp_stats) - 1)) == 0; }
 pwp_status status_of(cudaError_t e) { return e == cudaSuccess ? PWP_OK : PWP_ECUDA; }
 
 }  // namespace
@@ -41,7 +43,8 @@ pwp_status pwp_qk_norm_rope(const pwp_rope_args* a, void* stream) {
 
 static bool valid_attention(const pwp_attention_args* a) {
   if (!a || !valid_type(a->type) || a->n < 0 || a->nseq < 0 || a->hq < 1 || a->hk < 1 || a->hq % a->hk != 0 ||
-      a->d < 1 || a->d > 256 || a->n > 0x7fffffffLL / a->hq || a->nseq > (1 << 24) || !finite_f(a->scale))
+      a->d < 1 || a->d > 256 || a->n > 0x7fffffffLL / a->hq || a->nseq > (1 << 24) || !finite_f(a->scale) ||
+      !valid_stats(a->stats_dev))
     return false;
   for (int i = 0; i < 2; ++i)
     if (a->q_stride[i] < 0 || a->k_stride[i] < 0 || a->v_stride[i] < 0 || a->out_stride[i] < 0) return false;
@@ -66,7 +69,7 @@ static bool valid_linear(const pwp_linear_args* a) {
   if (!a || !valid_type(a->type) || a->rows < 0 || a->rows > 0x7fffffffLL || a->k < 1 || a->n < 1 ||
       a->k >= (1 << 24) || a->n >= (1 << 24) || a->activation < PWP_ACT_NONE || a->activation > PWP_ACT_GELU_TANH ||
       a->x_stride < 0 || a->w_stride < 0 || a->w_up_stride < 0 || a->residual_stride < 0 || a->out_stride < 0 ||
-      (!a->w_up_dev && a->bias_up_dev))
+      (!a->w_up_dev && a->bias_up_dev) || !valid_stats(a->stats_dev))
     return false;
   return a->rows == 0 || (a->x_dev && a->w_dev && a->out_dev && (a->rows == 1 || a->out_stride >= a->n));
 }

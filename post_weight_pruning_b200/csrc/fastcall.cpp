@@ -16,6 +16,7 @@
 #include <torch/version.h>
 
 #include <cmath>
+#include <cstdint>
 
 #include "pwp.h"
 
@@ -62,7 +63,7 @@ struct Call {
     const at::Tensor* t = any(o, 1, at::kByte);
     if (!t || t->size(0) != (int64_t)sizeof(pwp_stats)) return false;
     p = (pwp_stats*)t->data_ptr();
-    return true;
+    return ((uintptr_t)p & 7) == 0;
   }
   int32_t code() const { return type == at::kBFloat16 ? PWP_BF16 : PWP_FP32; }
   at::Tensor empty(at::IntArrayRef size) const {

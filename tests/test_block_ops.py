@@ -631,3 +631,31 @@ def test_a_gated_product_needs_both_weights(fake):
         with pytest.raises(TypeError, match="w_up"):
             pwp.gated_linear(z(2, 4), z(3, 4), None, **kw)
     assert not fake.calls
+
+
+def test_status_records_off_their_alignment_are_refused(fake):
+    """The kernels' atomics on one would fault; slices of a buffer of records at its multiples may be given."""
+    size = ctypes.sizeof(pwp.Stats)
+    buf = torch.zeros(3 * size + 64, dtype=torch.uint8)
+    at = -buf.data_ptr() % 64
+    for off in (1, 2, 4, size + 4):
+        rec = buf[at + off:at + off + size]
+        with pytest.raises(ValueError, match="stats"):
+            pwp.attention(z(2, 2, 4), z(2, 2, 4), z(2, 2, 4), CU, stats=rec)
+        with pytest.raises(ValueError, match="stats"):
+            pwp.linear(z(2, 4), z(3, 4), stats=rec)
+    assert not fake.calls
+    pwp.linear(z(2, 4), z(3, 4), stats=buf[at + size:at + 2 * size])
+    assert len([name for name, _ in fake.calls if name == "pwp_linear"]) == 1
+
+
+def test_c_entry_points_check_the_record():
+    L = pwp.lib()
+    a = AttentionArgs(q=256, k=256, v=256, out=256, cu_seqlens=256, stats=260, nseq=0, hq=1, hk=1, d=8, scale=1.0)
+    assert L.pwp_attention(bytes(a), None) == 1
+    a.stats = 264
+    assert L.pwp_attention(bytes(a), None) == 0                  # no sequences: nothing is enqueued
+    a = LinearArgs(rows=0, k=4, n=4, stats=260)
+    assert L.pwp_linear(bytes(a), None) == 1
+    a.stats = 264
+    assert L.pwp_linear(bytes(a), None) == 0
