@@ -143,21 +143,21 @@ def _check_tensor(t, name, shape, like, dtype=None):
 
 
 def _overlap(a, b):
-    """Whether the memory of two tensors may have an element in common.  Slices that interleave
+    """Whether the memory of two tensors may have a byte in common.  Slices that interleave
     (heads or columns of one packed buffer) are told apart by their places within a stride
     they share."""
-    e = a.element_size()
-    dims = [[(st * e, n) for st, n in zip(t.stride(), t.shape) if n != 1] for t in (a, b)]
+    sizes = [t.element_size() for t in (a, b)]
+    dims = [[(st * e, n) for st, n in zip(t.stride(), t.shape) if n != 1] for t, e in zip((a, b), sizes)]
     if any(n == 0 for ds in dims for _, n in ds):
         return False
-    reach = [sum(st * (n - 1) for st, n in ds) + e for ds in dims]
+    reach = [sum(st * (n - 1) for st, n in ds) + e for ds, e in zip(dims, sizes)]
     gap = b.data_ptr() - a.data_ptr()
     if gap >= reach[0] or -gap >= reach[1]:
         return False
     for pitch in {st for st, _ in dims[0]} & {st for st, _ in dims[1]}:
         if pitch == 0 or any(st > pitch and st % pitch for ds in dims for st, _ in ds):
             continue
-        inner = [sum(st * (n - 1) for st, n in ds if st < pitch) + e for ds in dims]
+        inner = [sum(st * (n - 1) for st, n in ds if st < pitch) + e for ds, e in zip(dims, sizes)]
         if inner[0] <= gap % pitch and gap % pitch + inner[1] <= pitch:
             return False
     return True
@@ -355,11 +355,11 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     if q_out is None:
         q_out = q.new_empty(q_shape)
     else:
-        _check_out(q_out, "q_out", q_shape, q, (k, q_weight, k_weight), q)
+        _check_out(q_out, "q_out", q_shape, q, (k, positions, freqs, q_weight, k_weight), q)
     if k_out is None:
         k_out = q.new_empty(k_shape)
     else:
-        _check_out(k_out, "k_out", k_shape, q, (q, q_out, q_weight, k_weight), k)
+        _check_out(k_out, "k_out", k_shape, q, (q, q_out, positions, freqs, q_weight, k_weight), k)
     if n and hq + hk:
         qs, ks, qos, kos = q.stride(), k.stride(), q_out.stride(), k_out.stride()
         _call("pwp_qk_norm_rope", ROPE_ARGS.pack(
@@ -411,7 +411,7 @@ def attention(q, k, v, cu_seqlens, *, causal=True, scale=None, out=None, stats=N
     if out is None:
         out = q.new_empty(q_shape)
     else:
-        _check_out(out, "out", q_shape, q, (q, k, v))
+        _check_out(out, "out", q_shape, q, (q, k, v, cu_seqlens, stats))
     nseq = cu_seqlens.shape[0] - 1
     if n and nseq:
         qs, ks, vs, os = q.stride(), k.stride(), v.stride(), out.stride()
@@ -448,7 +448,7 @@ def _linear(x, w, w_up, bias, bias_up, activation, residual, out, stats, name):
     if out is None:
         out = x.new_empty((rows, n))
     else:
-        _check_out(out, "out", (rows, n), x, (x, w, w_up, bias, bias_up), residual)
+        _check_out(out, "out", (rows, n), x, (x, w, w_up, bias, bias_up, stats), residual)
     if rows:
         xs, ws = x.stride(0), w.stride(0)
         us = w_up.stride(0) if w_up is not None else 0

@@ -659,3 +659,28 @@ def test_c_entry_points_check_the_record():
     assert L.pwp_linear(bytes(a), None) == 1
     a.stats = 264
     assert L.pwp_linear(bytes(a), None) == 0
+
+
+ROOM = torch.zeros(4096, dtype=torch.uint8)
+ROOM = ROOM[-ROOM.data_ptr() % 64:]
+OUT = ROOM[256:384].view(torch.bfloat16)                    # 64 elements
+
+
+@pytest.mark.parametrize("call", [
+    lambda at: pwp.qk_norm_rope(z(4, 2, 8), z(4, 2, 8), ROOM[at:at + 32].view(torch.int64), FR, q_out=OUT.view(4, 2, 8)),
+    lambda at: pwp.qk_norm_rope(z(4, 2, 8), z(4, 2, 8), ROOM[at:at + 32].view(torch.int64), FR, k_out=OUT.view(4, 2, 8)),
+    lambda at: pwp.qk_norm_rope(z(4, 2, 8), z(4, 2, 8), POS4, ROOM[at:at + 32].view(torch.float64), k_out=OUT.view(4, 2, 8)),
+    lambda at: pwp.attention(z(4, 2, 8), z(4, 2, 8), z(4, 2, 8), ROOM[at:at + 32].view(torch.int32), out=OUT.view(4, 2, 8)),
+    lambda at: pwp.attention(z(4, 2, 8), z(4, 2, 8), z(4, 2, 8), CU, stats=ROOM[at:at + ctypes.sizeof(pwp.Stats)],
+                             out=OUT.view(4, 2, 8)),
+    lambda at: pwp.linear(z(4, 8), z(16, 8), stats=ROOM[at:at + ctypes.sizeof(pwp.Stats)], out=OUT.view(4, 16)),
+])
+def test_outputs_over_what_the_call_reads_on_the_device_are_refused(fake, call):
+    """Positions, frequencies, offsets and the status record, whose elements have other sizes."""
+    for at in (232, 256, 352, 376):                   # 32 bytes or a record against bytes 256 .. 384
+        with pytest.raises(ValueError, match="overlaps"):
+            call(at)
+    assert not fake.calls
+    for at in (192, 384):
+        call(at)
+    assert len(fake.calls) >= 2
