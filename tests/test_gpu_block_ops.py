@@ -944,3 +944,55 @@ def test_attention_on_the_cuda_cores_several_tiles_a_cta(causal):
         at += length
     want, size = F.attention(np64(q[430:560]), np64(k[430:560]), np64(v[430:560]), [130], causal, spread=True)
     close(out[430:560], want, att_tol(q, k, lens, hq, 2, 20, want, size, "fp32"))
+
+
+def test_two_graphs_whose_attention_shares_its_work_out():
+    """Calls that take the counter's scratch, captured twice and replayed several times on two streams beside
+    each other and beside an eager call: each replay clears its own counter."""
+    torch, pwp = _torch(), _pwp()
+    from post_weight_pruning_b200 import block as B
+    lens = [1024] * 8
+    cases = [att_case(lens, 16, 8, 64, "bf16", 201 + 3 * i, extra=3) for i in range(3)]
+    q, k, v, cu = cases[0]
+    args = B.ATTENTION_ARGS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), q.data_ptr(), *q.stride()[:2], *k.stride()[:2],
+                                 *v.stride()[:2], *q.stride()[:2], cu.data_ptr(), 0, q.shape[0], len(lens), pwp.BF16, 16, 8, 64,
+                                 1, 0.125, 0, 0)
+    assert pwp.lib().pwp_attention_workspace_bytes(args) > 0
+    want = [pwp.attention(*c)[:8192].clone() for c in cases]
+    outs = [torch.empty_like(c[0]) for c in cases]
+    for o, c in zip(outs, cases):                        # the first call of each stream's pool is not a captured one
+        pwp.attention(*c, out=o)
+    torch.cuda.synchronize()
+    graphs, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    for o, c in zip(outs[:2], cases):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pwp.attention(*c, out=o)
+        graphs.append(g)
+    for _ in range(6):
+        for o in outs:
+            o.fill_(7.0)
+        torch.cuda.synchronize()
+        for _ in range(2):                               # each graph twice in a row
+            for g, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+            pwp.attention(*cases[2], out=outs[2])
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o[:8192], w) and bool((o[8192:] == 7.0).all())
+
+
+def test_operators_repeat_themselves_exactly():
+    """The same bits call after call, whichever CTA took which work."""
+    torch, pwp = _torch(), _pwp()
+    q, k, v, cu = att_case([1500, 3, 700, 64, 900], 16, 4, 128, "bf16", 211)
+    calls = [lambda: pwp.attention(q, k, v, cu), lambda: pwp.attention(q.float(), k.float(), v.float(), cu)]
+    for rows, kk, n in ((1, 4096, 1000), (37, 2000, 1544), (300, 1024, 1000), (3000, 512, 1032)):
+        x, w, u = rnd((rows, kk), "bf16", 212), rnd((n, kk), "bf16", 213, 0.05), rnd((n, kk), "bf16", 214, 0.05)
+        calls += [lambda x=x, w=w: pwp.linear(x, w), lambda x=x, w=w, u=u: pwp.gated_linear(x, w, u),
+                  lambda x=x, w=w: pwp.linear(x.float(), w.float())]
+    for i, call in enumerate(calls):
+        first = call()
+        for _ in range(5):
+            assert torch.equal(call(), first), i
