@@ -180,18 +180,23 @@ def _check_out(t, name, shape, like, others, same=None):
     for x in (*others, same):
         if x is not None and _overlap(t, x):
             raise ValueError(f"{name}: overlaps a tensor the call reads or writes")
-    _forward_only(t)
+    _check_plain(t)
 
 
-def _forward_only(*ts):
+def _check_plain(*ts):
+    """Refuses tensors that are more than their memory: with a gradient or a forward-mode tangent to
+    carry on, or a negation that is still to be done."""
     torch = _torch()
     recording, forward = torch.is_grad_enabled(), torch.autograd.forward_ad
     dual = forward._current_level >= 0
     for t in ts:
-        if t is not None and ((recording and t.requires_grad) or
-                              (dual and forward.unpack_dual(t).tangent is not None)):
+        if t is None:
+            continue
+        if (recording and t.requires_grad) or (dual and forward.unpack_dual(t).tangent is not None):
             raise ValueError("the operators compute a forward pass only: call them under torch.no_grad() "
                              "or on detached tensors, without forward-mode tangents")
+        if t.is_neg():
+            raise ValueError("a negated view (of a conjugate's imaginary part): resolve_neg() gives its values")
 
 
 def _ptr(t):
@@ -233,7 +238,7 @@ def rms_norm(x, weight=None, *, eps=1e-5, out=None, stream=None):
         _check_tensor(weight, "weight", (width,), x)
     if not 0 <= eps < math.inf:
         raise ValueError(f"eps: {eps}")
-    _forward_only(x, weight)
+    _check_plain(x, weight)
     if out is None:
         out = x.new_empty(shape)
     else:
@@ -351,7 +356,7 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
         _check_tensor(q_weight, "q_weight", (d,), q)
     if k_weight is not None:
         _check_tensor(k_weight, "k_weight", (d,), q)
-    _forward_only(q, k, freqs, q_weight, k_weight)
+    _check_plain(q, k, freqs, q_weight, k_weight)
     if q_out is None:
         q_out = q.new_empty(q_shape)
     else:
@@ -406,7 +411,7 @@ def attention(q, k, v, cu_seqlens, *, causal=True, scale=None, out=None, stats=N
         scale = d ** -0.5
     elif not math.isfinite(scale):
         raise ValueError(f"scale: {scale}")
-    _forward_only(q, k, v)
+    _check_plain(q, k, v)
     stats_p = _stats_ptr(stats, q)
     if out is None:
         out = q.new_empty(q_shape)
@@ -443,7 +448,7 @@ def _linear(x, w, w_up, bias, bias_up, activation, residual, out, stats, name):
         raise ValueError(f"activation: {activation!r}, one of {sorted(ACTIVATIONS)} expected")
     if residual is not None:
         _check_tensor(residual, "residual", (rows, n), x)
-    _forward_only(x, w, w_up, bias, bias_up, residual)
+    _check_plain(x, w, w_up, bias, bias_up, residual)
     stats_p = _stats_ptr(stats, x)
     if out is None:
         out = x.new_empty((rows, n))

@@ -684,3 +684,17 @@ def test_outputs_over_what_the_call_reads_on_the_device_are_refused(fake, call):
     for at in (192, 384):
         call(at)
     assert len(fake.calls) >= 2
+
+
+def test_negated_views_are_refused(fake):
+    """Their memory holds the values with the other sign."""
+    x = torch.zeros(2, 1, dtype=torch.complex64).conj().imag
+    assert x.is_neg()
+    f = lambda *shape: z(*shape, dtype=torch.float32)
+    for call in (lambda: pwp.rms_norm(x), lambda: pwp.rms_norm(f(2, 1), out=x), lambda: pwp.linear(x, f(3, 1)),
+                 lambda: pwp.linear(f(4, 1), x), lambda: pwp.attention(f(2, 1, 1), x[:, None], f(2, 1, 1), CU)):
+        with pytest.raises(ValueError, match="negated"):
+            call()
+    assert not fake.calls
+    pwp.rms_norm(x.resolve_neg())
+    assert len(fake.calls) == 1
