@@ -34,22 +34,25 @@ __device__ __forceinline__ float normal_tail(float a) {
   return p * t * __expf(-0.5f * a * a);
 }
 
-// x / (1 + e^-z), z of the sign of x.  e^-|z| never overflows, so results far below zero keep
-// their value down to the smallest numbers (e^-z is infinite from z = -88.7 on, where
-// x e^z is still a normal number).  bf16 takes the fast exponential (off by 2 + 1.17 |z| steps
-// of 2^-23, a hundredth of bf16's half step at |z| = 88) and division (the divisor lies in [1, 2]).
+// x / (1 + e^-z), z of the sign of x, as x (e^z / (1 + e^z)).  z is cut at 60, where the fraction
+// is 1 to the last bit, so e^z never overflows and results far below zero keep their value
+// down to the smallest numbers (e^-z is infinite from z = -88.7 on, where x e^z is still a normal
+// number).  bf16 takes the fast exponential (off by 2 + 1.17 |z| steps of 2^-23, a hundredth
+// of bf16's half step at |z| = 88); the division is good for divisors up to 2^126 (a full one calls
+// a routine, which cost the fp32 kernel's main loop registers: 1024 x 8192 x 4096 1710 us, 1635
+// this way).
 template <typename T>
 __device__ __forceinline__ float times_logistic(float x, float z) {
-  const float e = sizeof(T) == 4 ? expf(-fabsf(z)) : __expf(-fabsf(z));
-  const float num = z < 0.f ? x * e : x;
-  return sizeof(T) == 4 ? num / (1.f + e) : __fdividef(num, 1.f + e);
+  z = fminf(z, 60.f);
+  const float e = sizeof(T) == 4 ? expf(z) : __expf(z);
+  return x * __fdividef(e, 1.f + e);
 }
 
 // Activations of pwp_activation in fp32, for results of type T.
 //
 // erf-GELU: 1 + erf(x / sqrt 2) would cancel below zero (nothing is left from x = -5.8 on), so
 // fp32 takes erfc, and bf16, whose half step is 2^-8, normal_tail: 16384 x 128 x 8192, where the epilogue
-// is the bound, takes 202 us with it, 208 with erff and 392 with erfcf.
+// is the bound, takes 209 us with it, 208 with erff and 392 with erfcf.
 template <typename T>
 __device__ __forceinline__ float activate(int act, float x) {
   switch (act) {

@@ -353,8 +353,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
       // 31.5 us with a row per thread, 13.8 this way).
       const int prow = lane >> 2, pcol = lane & 3, brow = lane >> 4, bcol = 2 * (lane & 15);
 #pragma unroll 1
-      for (int ch = part * (NT / 128); ch < (part + 1) * (NT / 128); ++ch) {
-        const int c0 = c * NT + ch * 32, avail = n - c0;
+      for (int i32 = 0; i32 < NT / 128; ++i32) {
+        const int ch = part * (NT / 128) + i32, c0 = c * NT + ch * 32, avail = n - c0;
         if (avail <= 0) break;
         const bool on = 8 * pcol < avail;
         if (ep.vec && ep.residual) {

@@ -809,10 +809,10 @@ def test_gelu_in_the_tails(lo, hi, dtype):
                                        ("gelu_tanh", -10.5, -5.0), ("gelu_tanh", 5.0, 200.0)])
 def test_logistic_activations_in_the_tails(act, lo, hi, dtype):
     """x / (1 + e^-z) relative to itself, z = x (SiLU) or 2 sqrt(2/pi) (x + 0.044715 x^3), which is off by 6
-    half steps (four operations, two constants): |z| 6 2^-24 of the result.  fp32: the exponential to 2
-    steps (documented: 1), the sum, product and quotient to half a step each.  bf16: the exponential
-    to 2 + 1.173 |z| steps and the quotient to 2 (documented).  Exponentials below the least normal
-    number (2^-126) are off by 2^-149."""
+    half steps (four operations, two constants): |z| 6 2^-24 of the result.  fp32: the exponential to 1
+    step (its documented bound), the sum and product to half a step each, the quotient to 2
+    (documented).  bf16: the exponential to 2 + 1.173 |z| steps (documented), the others as in fp32.
+    Exponentials below the least normal number (2^-126) are off by 2^-149."""
     def z(t):
         return t if act == "silu" else 2 * math.sqrt(2 / math.pi) * (t + 0.044715 * t ** 3)
 
