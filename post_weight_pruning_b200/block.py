@@ -8,10 +8,11 @@ the rotation's frequencies.  ``block_forward`` runs them as a decoder block and 
 distinct layer input beside the block's output, and ``prune_decoder_block`` prunes the block
 with those inputs and passes the hidden states through the pruned layers.
 
-The operators run on the device of their tensors and on the given or the current stream of
-that device; nothing synchronises and nothing is kept between calls.  They compute a forward
-pass only: an input that requires a gradient is refused while gradients are recorded, and
-one that carries a forward-mode tangent always.
+They run on the device of their tensors and on the given or the current stream of that device,
+and nothing is kept between calls.  The operators do not synchronise; ``block_forward`` copies the
+sequences' offsets, and positions that are not given, from the host and waits for each copy.
+They compute a forward pass only: an input that requires a gradient is refused while
+gradients are recorded, and one that carries a forward-mode tangent always.
 """
 from __future__ import annotations
 

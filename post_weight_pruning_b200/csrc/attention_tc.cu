@@ -3,7 +3,8 @@
 //
 //   o_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = 2^(c (s_ij - m_i)),  s = q k^T,  c = scale log2(e)
 //
-// in one pass over the keys, 128 at a time, with a reference m_i that is the running maximum
+// in one pass over the keys, 128 at a time (the online softmax of Milakov and Gimelshein, with its
+// rescaling put off), with a reference m_i that is the running maximum
 // or lags behind it by at most 8 in the exponent: o and the sum are rescaled only when the
 // maximum has grown by more (p then stays below 2^8, far from any overflow, and bf16 keeps
 // its relative precision).
@@ -24,13 +25,20 @@
 // S_w(j) becoming full implies that O_w holds block j-1's product (the MMAs of a thread complete
 // in order), so a softmax thread may rescale its row of O_w without another barrier.
 //
-// What bounds it (16 x 2048 tokens, 32 heads of 128: 0.62 ms causal, 0.95 ms full, 890 and 1155
-// TFLOP/s, back to back for seconds 0.72 ms under the power cap): a tile's chain of softmax (about 1700 cycles per 128 keys: 1024 of exponentials at
-// 16 a cycle and SM, the rest issue and latency), its two MMA groups of 512 and the hand-overs
-// between them, which the other tile fills only in part; the tensor core works two thirds of
-// the time.  The single-thread roles are bound by instruction issue and fetch, so they hold
-// little code: running slots and descriptors and no item search were worth 0.09 ms of 0.70.
-// Tried and slower (full attention): P handed over in halves (1.24 ms, and 1.15 with an MMA warp
+// P is rounded to bf16 (2^-8 of each at most) because the tensor core takes both operands in one
+// type, V's: the output's error against 64 bits grows from 0.0016 to 0.0021 of its size (the
+// output's own rounding is 0.0016).  Scores, statistics, sums and O are fp32; the sum adds the
+// probabilities before that rounding.  The products accumulate in the tensor core, which truncates.
+//
+// What bounds it (16 x 2048 tokens, 32 heads of 128: causal 632 us twenty in a row, 736 a thousand in a
+// row under the power cap, 870 and 750 TFLOP/s; full 1.07 and 1.15 ms, 1025 and 955): a tile's chain of
+// softmax (about 1700 cycles per 128 keys: 900 of exponentials at 16 a cycle and SM, seven eighths of
+// them, the rest issue and latency), its two MMA groups of 512 and the hand-overs between them, which
+// the other tile fills only in part: the tensor pipe is busy 38 % of the time causal and
+// 52 % full (profiled at 4 x 2048, caches cold).  The single-thread roles are bound by
+// instruction issue and fetch, so they hold little code: running slots and descriptors and no item
+// search were worth 0.09 ms of 0.70.
+// Tried and slower (full attention, when it took 0.95 ms): P handed over in halves (1.24 ms, and 1.15 with an MMA warp
 // per tile); blocks of 64 keys with two S per tile (1.42); 32 keys at a time (1.31); two threads
 // to a row, 16 softmax warps of 104 registers (1.09); the sum in
 // place of the maximum as the reference's guard (0.99); none (0.97) or three of eight pairs of
@@ -230,7 +238,7 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// 2^x of two values on the FMA pipe: x = n + f with n the nearest whole number, f in [-1/2, 1/2],
+// 2^x of two values on the FMA pipe, after Cody and Waite: x = n + f with n the nearest whole number, f in [-1/2, 1/2],
 // and 2^f by the cubic 1 + f (a + f (b + f c)) of least largest relative error (found by linear
 // programming over 4001 points: 1.02e-4 = 2^-13.3, a fortieth of a bf16 half step).  The
 // constant term is exactly 1, so x clamped at -127 gives exactly 0 (1's exponent field of 127,

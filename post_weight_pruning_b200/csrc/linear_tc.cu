@@ -16,10 +16,13 @@
 // over the CTAs of a cluster so that every SM streams weights.  Each CTA then stores its
 // partial sums straight from tensor memory into the shared memory of the CTA that finishes
 // those rows (stores do not wait for the other side, loads from it would), which adds them
-// in rank order -- no atomics, no workspace.  One row of 4096 x 4096 bf16 weights:
-// 10.4 us (5.1 at the copy rate), 33 rows of two 11008 x 4096: 33.0 us (27.6).
+// in rank order -- no atomics, no workspace.  One row of 4096 x 4096 bf16 weights: 11.3 us a call
+// on fresh data (5.1 at the copy rate), 8.9 replayed with the weights in L2; 33 rows of two
+// 11008 x 4096: 37.9 us a call, 32.2 replayed (27.6).
 //
-// Accumulators are fp32; bias, activation, product and residual are applied in fp32 and the
+// Accumulators are fp32, but the tensor core truncates when it adds: over 11008 terms 6 in 1000
+// outputs are rounded to bf16 the other way than a plain fp32 sum's, and the error against 64 bits
+// stays that of the rounding (0.00166 of the size).  Bias, activation, product and residual are applied in fp32 and the
 // result is rounded to bf16 once.  Every wait is bounded: a wait that runs out records
 // PWP_ETIMEOUT and the rows concerned come out NaN; copies and MMAs in flight are waited for
 // before a CTA leaves.
@@ -348,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
       // writes; turned through shared memory (16-byte pieces swizzled by row) a warp writes, and
       // reads of the residual, eight rows' whole 64 bytes.  Sixteen warps, because each spends
       // most of its time waiting: at 16384 x 128 x 8192, where the epilogue is the bound, plain
-      // 108 us with eight warps of 64 columns and 89-96 with these, with erf-GELU 300 and 190-199.
+      // 108 us with eight warps of 64 columns and 97 with these, with erf-GELU 300 and 209.
       // Rows that are not 16-byte aligned go two at a time, 4 or 2 bytes a store (8000 x 1000 x 300:
       // 31.5 us with a row per thread, 13.8 this way).
       const int prow = lane >> 2, pcol = lane & 3, brow = lane >> 4, bcol = 2 * (lane & 15);

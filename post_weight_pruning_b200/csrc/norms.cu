@@ -15,8 +15,15 @@
 // registers.  Warps are independent: each takes a token's heads a few at a time, the next ones'
 // loads in flight meanwhile; several tokens at once when they have few heads; a share of a
 // token's heads when there are few tokens.  Other head sizes go through shared memory, a warp
-// per head.  16384 tokens, 64 heads of
-// 128 (512 MB): 96 us, 5.6 TB/s.
+// per head.
+//
+// Measured.  rms_norm, 32768 rows: 4096 bf16 90 us (5.9 TB/s), 4096 fp32 160 us (6.7); rows that are
+// not 16-byte aligned, 4097 bf16 124 us (4.3), and long ones, 16384 x 20000 bf16 552 us (2.4), are
+// read twice.  qk_norm_rope, 16384 tokens without and with head norms: 32 + 32 heads of 128 bf16 93
+// and 110 us (5.8 and 4.9 TB/s), 32 + 8 bf16 63 and 76 (5.4 and 4.4), 32 + 8 fp32 107 and 124 (6.3 and
+// 5.4), 4 + 1 of 96 bf16 19 and 27 (1.7 and 1.2), 4 + 1 of 96 fp32 20 and 35 (3.2 and 1.8).  With few heads
+// a warp's chain of position, angle, sine and one round of heads bounds it, with norms the sums
+// over a head's lanes, one shuffle after another.
 #include "block_ops.cuh"
 
 namespace pwp {
